@@ -25,6 +25,7 @@
 #include "../../include/gemm355.h"
 #include "kernels.h"
 #include "plan.h"
+#include "serve.h"
 #include "tiles.h"
 
 using namespace g355;
@@ -473,9 +474,345 @@ gemm355_status conv_setup(const gemm355_conv_args *c, gemm355_args &a, ConvShape
     return GEMM355_OK;
 }
 
+/* ---- serving operators: argument checks ---- */
+
+const int64_t kMaxDim = (int64_t)1 << 30;
+
+/* Extent in bytes of `rows` rows of `cols` elements, ld elements apart. */
+struct Span {
+    uintptr_t lo, hi;
+    Span(const void *ptr, uint64_t bytes) : lo((uintptr_t)ptr), hi((uintptr_t)ptr + (ptr ? bytes : 0)) {}
+    Span(const void *ptr, int64_t rows, int64_t cols, int64_t ld, int64_t es)
+        : Span(ptr, rows > 0 && cols > 0 ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * (uint64_t)es : 0)
+    {
+    }
+    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi && lo < hi && o.lo < o.hi; }
+};
+
+bool aligned(const void *ptr, uintptr_t to) { return ((uintptr_t)ptr & (to - 1)) == 0; }
+
+gemm355_status check_w4(const gemm355_w4_matrix *q, W4Params &w)
+{
+    if (!q || q->N < 0 || q->K < 0) return GEMM355_EINVAL;
+    if (q->fmt != GEMM355_W4_INT && q->fmt != GEMM355_W4_MXFP4) return GEMM355_EINVAL;
+    const bool mx = q->fmt == GEMM355_W4_MXFP4;
+    if (mx ? q->group != 32 : q->group != 32 && q->group != 64 && q->group != 128) return GEMM355_EINVAL;
+    if (mx && q->zeros) return GEMM355_EINVAL;
+    if (q->N > kMaxDim || q->K > kMaxDim || q->N * q->K > ((int64_t)1 << 40)) return GEMM355_EUNSUPPORTED;
+    const int64_t ldw = q->ldw ? q->ldw : (q->K + 31) / 32 * 32;
+    if (ldw < q->K || ldw % 32 != 0) return GEMM355_EINVAL;
+    if (ldw > kMaxDim) return GEMM355_EUNSUPPORTED;
+    if (q->N > 0 && q->K > 0 && (!q->codes || !q->scales)) return GEMM355_EINVAL;
+    if (!aligned(q->codes, 16) || (!mx && !aligned(q->scales, 2))) return GEMM355_EALIGN;
+    w.codes = q->codes;
+    w.ldb = ldw / 2;
+    w.scales = q->scales;
+    w.zeros = q->zeros;
+    w.N = (int32_t)q->N;
+    w.K = (int32_t)q->K;
+    w.group = q->group;
+    w.ng = (int32_t)((q->K + q->group - 1) / q->group);
+    w.mx = mx ? 1 : 0;
+    return GEMM355_OK;
+}
+
+/* Whether any part of the matrix lies in s. */
+bool w4_meets(const W4Params &w, const Span &s)
+{
+    const int64_t groups = (int64_t)w.N * w.ng;
+    return s.meets(Span(w.codes, w.N, ((int64_t)w.K + 31) / 32 * 16, w.ldb, 1)) ||
+           s.meets(Span(w.scales, (uint64_t)groups * (w.mx ? 1 : 2))) || s.meets(Span(w.zeros, (uint64_t)groups));
+}
+
+gemm355_status w4_convert(const gemm355_w4_matrix *q, const void *dense, int64_t ld, gemm355_src type, W4QuantParams &p)
+{
+    gemm355_status st = check_w4(q, p.w);
+    if (st != GEMM355_OK) return st;
+    if (type != GEMM355_SRC_F32 && type != GEMM355_SRC_BF16) return GEMM355_EINVAL;
+    const int64_t es = type == GEMM355_SRC_F32 ? 4 : 2;
+    p.ld = ld ? ld : q->K;
+    if (p.ld < q->K) return GEMM355_EINVAL;
+    if (p.ld > kMaxDim) return GEMM355_EUNSUPPORTED;
+    if (q->N > 0 && q->K > 0 && !dense) return GEMM355_EINVAL;
+    if (!aligned(dense, (uintptr_t)es)) return GEMM355_EALIGN;
+    if (w4_meets(p.w, Span(dense, q->N, q->K, p.ld, es))) return GEMM355_EINVAL;
+    p.x = dense;
+    p.y = const_cast<void *>(dense);
+    p.f32 = es == 4 ? 1 : 0;
+    p.vec = aligned(dense, 16) && p.ld * es % 16 == 0 ? 1 : 0;
+    return GEMM355_OK;
+}
+
+gemm355_status check_kv(const gemm355_kv_cache &c, KvParams &k)
+{
+    if (c.pages < 1 || c.heads < 1 || c.batch < 0 || c.tokens < 0 || c.max_new < 1 || c.max_len < 0 || c.table_ld < 0)
+        return GEMM355_EINVAL;
+    if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return GEMM355_EUNSUPPORTED;
+    if (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128) return GEMM355_EUNSUPPORTED;
+    if (c.pages > 0x7FFFFFFF || c.tokens > kMaxDim || c.max_new > kMaxDim || c.max_len > kMaxDim || c.table_ld > kMaxDim ||
+        c.batch > 65535 || c.batch * c.heads > 65535)
+        return GEMM355_EUNSUPPORTED;
+    const int64_t ld = c.table_ld ? c.table_ld : (c.max_len + c.page - 1) / c.page;
+    if (c.max_len > ld * c.page) return GEMM355_EINVAL;
+    if (!c.q_start && c.tokens != c.batch * c.max_new) return GEMM355_EINVAL;
+    if (!c.k || !c.v || !c.k_scale || !c.v_scale) return GEMM355_EINVAL;
+    if (c.batch > 0 && ((!c.table && c.max_len > 0) || !c.lens)) return GEMM355_EINVAL;
+    if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.table, 4) || !aligned(c.lens, 4) || !aligned(c.q_start, 4))
+        return GEMM355_EALIGN;
+    k.k = c.k;
+    k.v = c.v;
+    k.k_scale = c.k_scale;
+    k.v_scale = c.v_scale;
+    k.table = c.table;
+    k.lens = c.lens;
+    k.q_start = c.q_start;
+    k.pages = c.pages;
+    k.table_ld = ld;
+    k.H = c.heads;
+    k.page = c.page;
+    k.page_log2 = c.page == 16 ? 4 : c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
+    k.B = (int32_t)c.batch;
+    k.tokens = (int32_t)c.tokens;
+    /* no sequence has more new rows than the step has */
+    k.max_new = (int32_t)std::min(c.max_new, std::max<int64_t>(c.tokens, 1));
+    k.max_len = (int32_t)c.max_len;
+    return GEMM355_OK;
+}
+
+/* Whether any buffer of the cache, or of the step's indices, lies in s. */
+bool kv_meets(const gemm355_kv_cache &c, const Span &s, bool indices)
+{
+    const uint64_t blocks = (uint64_t)c.pages * (uint64_t)c.heads, bytes = blocks * (uint64_t)c.page * (uint64_t)c.head_dim;
+    if (s.meets(Span(c.k, bytes)) || s.meets(Span(c.v, bytes)) || s.meets(Span(c.k_scale, blocks)) || s.meets(Span(c.v_scale, blocks)))
+        return true;
+    const int64_t ld = c.table_ld ? c.table_ld : (c.max_len + c.page - 1) / c.page;
+    return indices && (s.meets(Span(c.table, (uint64_t)(c.batch * ld * 4))) || s.meets(Span(c.lens, (uint64_t)c.batch * 4)) ||
+                       s.meets(Span(c.q_start, (uint64_t)(c.batch + 1) * 4)));
+}
+
+/* A step's bf16 rows of `heads` heads. */
+gemm355_status check_rows(const void *ptr, int64_t &ld, int64_t tokens, int64_t heads, int32_t dim)
+{
+    const int64_t width = heads * dim;
+    if (!ld) ld = width;
+    if (heads < 1 || ld < width || ld % 8 != 0) return GEMM355_EINVAL;
+    if (width > kMaxDim || ld > kMaxDim) return GEMM355_EUNSUPPORTED;
+    if (tokens > 0 && !ptr) return GEMM355_EINVAL;
+    return aligned(ptr, 16) ? GEMM355_OK : GEMM355_EALIGN;
+}
+
+gemm355_status append_setup(const gemm355_kv_append_args *a, KvAppendParams &p)
+{
+    if (!a) return GEMM355_EINVAL;
+    const gemm355_kv_cache &c = a->cache;
+    gemm355_status st = check_kv(c, p.c);
+    if (st != GEMM355_OK) return st;
+    p.ldk = a->ldk;
+    p.ldv = a->ldv;
+    p.ldq = a->ldq;
+    p.ldqo = a->ldqo;
+    if ((st = check_rows(a->k, p.ldk, c.tokens, c.heads, c.head_dim)) != GEMM355_OK) return st;
+    if ((st = check_rows(a->v, p.ldv, c.tokens, c.heads, c.head_dim)) != GEMM355_OK) return st;
+    if ((a->q == nullptr) != (a->q_out == nullptr)) return GEMM355_EINVAL;
+    if (a->q) {
+        if ((st = check_rows(a->q, p.ldq, c.tokens, a->q_heads, c.head_dim)) != GEMM355_OK) return st;
+        if ((st = check_rows(a->q_out, p.ldqo, c.tokens, a->q_heads, c.head_dim)) != GEMM355_OK) return st;
+    }
+    if (a->rot_dim < 0 || a->rot_dim > c.head_dim || a->rot_dim % 2 != 0) return GEMM355_EINVAL;
+    if (a->rot_dim) {
+        if (a->rot_len < c.max_len || (c.max_len > 0 && (!a->cos || !a->sin))) return GEMM355_EINVAL;
+        if (!aligned(a->cos, 4) || !aligned(a->sin, 4)) return GEMM355_EALIGN;
+    }
+    const int64_t kw = (int64_t)c.heads * c.head_dim, qw = (int64_t)a->q_heads * c.head_dim;
+    const Span k(a->k, c.tokens, kw, p.ldk, 2), v(a->v, c.tokens, kw, p.ldv, 2), q(a->q, c.tokens, qw, p.ldq, 2);
+    const Span out(a->q_out, c.tokens, qw, p.ldqo, 2);
+    const uint64_t table = a->rot_dim ? (uint64_t)c.max_len * (uint64_t)(a->rot_dim / 2) * 4 : 0;
+    const Span cs(a->cos, table), sn(a->sin, table);
+    const int64_t ld = p.c.table_ld;
+    const Span idx[3] = {Span(c.table, (uint64_t)(c.batch * ld * 4)), Span(c.lens, (uint64_t)c.batch * 4),
+                         Span(c.q_start, (uint64_t)(c.batch + 1) * 4)};
+    if (out.meets(k) || out.meets(v) || out.meets(q) || out.meets(cs) || out.meets(sn) || kv_meets(c, out, true)) return GEMM355_EINVAL;
+    if (kv_meets(c, k, false) || kv_meets(c, v, false) || kv_meets(c, q, false) || kv_meets(c, cs, false) || kv_meets(c, sn, false) ||
+        kv_meets(c, idx[0], false) || kv_meets(c, idx[1], false) || kv_meets(c, idx[2], false))
+        return GEMM355_EINVAL;
+    const int64_t each = ((int64_t)p.c.max_new + c.page - 2) / c.page + 1;
+    const int64_t q_blocks = a->q ? ((int64_t)p.c.max_new * a->q_heads * (c.head_dim / 8) + 255) / 256 : 0;
+    if (each > kMaxDim / (2 * std::max<int64_t>(1, c.batch * c.heads)) || q_blocks > kMaxDim / std::max<int64_t>(1, c.batch))
+        return GEMM355_EUNSUPPORTED;
+    p.xk = (const uint16_t *)a->k;
+    p.xv = (const uint16_t *)a->v;
+    p.q = (const uint16_t *)a->q;
+    p.q_out = (uint16_t *)a->q_out;
+    p.cos = a->cos;
+    p.sin = a->sin;
+    p.Hq = a->q_heads;
+    p.D = c.head_dim;
+    p.rot = a->rot_dim;
+    p.interleaved = a->interleaved ? 1 : 0;
+    return GEMM355_OK;
+}
+
+/* Checks, the split of the key axis and the scratch of an attention call. */
+gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, size_t &bytes)
+{
+    if (!a) return GEMM355_EINVAL;
+    const gemm355_kv_cache &c = a->cache;
+    gemm355_status st = check_kv(c, p.c);
+    if (st != GEMM355_OK) return st;
+    if (a->q_heads < 1 || a->q_heads % c.heads != 0 || a->window < 0 || a->sinks < 0 || a->splits < 0) return GEMM355_EINVAL;
+    if (!(a->scale >= 0.0f) || !(a->scale <= 3.0e38f)) return GEMM355_EINVAL;
+    p.ldq = a->ldq;
+    p.ldo = a->ldo;
+    if ((st = check_rows(a->q, p.ldq, c.tokens, a->q_heads, c.head_dim)) != GEMM355_OK) return st;
+    if ((st = check_rows(a->o, p.ldo, c.tokens, a->q_heads, c.head_dim)) != GEMM355_OK) return st;
+    if (!aligned(a->lse, 4)) return GEMM355_EALIGN;
+    const int64_t qw = (int64_t)a->q_heads * c.head_dim;
+    const Span q(a->q, c.tokens, qw, p.ldq, 2), o(a->o, c.tokens, qw, p.ldo, 2), lse(a->lse, (uint64_t)(c.tokens * a->q_heads * 4));
+    if (o.meets(q) || o.meets(lse) || lse.meets(q) || kv_meets(c, o, true) || kv_meets(c, lse, true)) return GEMM355_EINVAL;
+    p.q = (const uint16_t *)a->q;
+    p.o = (uint16_t *)a->o;
+    p.lse = a->lse;
+    p.scale_log2 = (float)((a->scale > 0.0f ? (double)a->scale : 1.0 / sqrt((double)c.head_dim)) * 1.4426950408889634);
+    p.Hq = a->q_heads;
+    p.group = a->q_heads / c.heads;
+    p.D = c.head_dim;
+    p.window = a->window >= c.max_len ? 0 : (int32_t)a->window;
+    p.sinks = (int32_t)std::min<int64_t>(a->sinks, c.max_len);
+    const int64_t rows = (int64_t)p.c.max_new * p.group;
+    if (rows > (int64_t)16 * 65535) return GEMM355_EUNSUPPORTED;
+    p.row_tiles = (int32_t)((rows + 15) / 16);
+    const int64_t tiles = std::max<int64_t>(1, c.batch * c.heads * p.row_tiles);
+    int64_t seen = c.max_len;
+    if (p.window) seen = std::min(seen, (int64_t)p.window + p.c.max_new + p.sinks + 128);
+    const int64_t most = std::max<int64_t>(1, (seen + 255) / 256);
+    const int32_t cus = [] {
+        int n = 0;
+        if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
+            (void)hipGetLastError();
+            return 256;
+        }
+        return device_cus();
+    }();
+    const int64_t want = a->splits ? a->splits : (2 * (int64_t)cus + tiles - 1) / tiles;
+    p.splits = (int32_t)std::min(want, most);
+    const int64_t slots = tiles * p.splits;
+    bytes = p.splits > 1 ? (size_t)slots * 16 * (size_t)(p.D + 2) * sizeof(float) : 0;
+    p.part = p.stat = nullptr;
+    return GEMM355_OK;
+}
+
+/* Whether work enqueued on the stream goes into a graph. */
+bool capturing(void *stream)
+{
+    if (!stream) return false;
+    hipStreamCaptureStatus state = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing((hipStream_t)stream, &state) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    return state != hipStreamCaptureStatusNone;
+}
+
 } /* namespace */
 
 extern "C" {
+
+gemm355_status gemm355_w4_quantize(const void *w, int64_t ld, gemm355_src src, const gemm355_w4_matrix *q, void *stream)
+{
+    W4QuantParams p;
+    const gemm355_status st = w4_convert(q, w, ld, src, p);
+    if (st != GEMM355_OK || q->N == 0 || q->K == 0) return st;
+    return launch_w4_quantize(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+}
+
+gemm355_status gemm355_w4_dequantize(const gemm355_w4_matrix *q, void *w, int64_t ld, gemm355_src dst, void *stream)
+{
+    W4QuantParams p;
+    const gemm355_status st = w4_convert(q, w, ld, dst, p);
+    if (st != GEMM355_OK || q->N == 0 || q->K == 0) return st;
+    return launch_w4_dequantize(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+}
+
+gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx, const gemm355_w4_matrix *w, void *y, int64_t ldy,
+                               gemm355_src out, void *stream)
+{
+    W4GemmParams p;
+    const gemm355_status st = check_w4(w, p.w);
+    if (st != GEMM355_OK) return st;
+    if (M < 0 || (out != GEMM355_SRC_F32 && out != GEMM355_SRC_BF16)) return GEMM355_EINVAL;
+    if (M > ((int64_t)1 << 19)) return GEMM355_EUNSUPPORTED;
+    const int64_t N = w->N, K = w->K, es = out == GEMM355_SRC_F32 ? 4 : 2;
+    p.ldx = ldx ? ldx : K;
+    p.ldy = ldy ? ldy : N;
+    if (p.ldx < K || p.ldy < N) return GEMM355_EINVAL;
+    if (p.ldx > kMaxDim || p.ldy > kMaxDim) return GEMM355_EUNSUPPORTED;
+    if (M > 0 && N > 0 && (!y || (K > 0 && !x))) return GEMM355_EINVAL;
+    if (!aligned(x, 2) || !aligned(y, (uintptr_t)es)) return GEMM355_EALIGN;
+    const Span ys(y, M, N, p.ldy, es);
+    if (ys.meets(Span(x, M, K, p.ldx, 2)) || w4_meets(p.w, ys)) return GEMM355_EINVAL;
+    if (M == 0 || N == 0) return GEMM355_OK;
+    if (K == 0)
+        return launch_zero(y, (int32_t)M, (int32_t)N, p.ldy, 0, 1, (int32_t)es, (hipStream_t)stream) == hipSuccess ? GEMM355_OK
+                                                                                                                  : GEMM355_EHIP;
+    p.x = (const uint16_t *)x;
+    p.y = y;
+    p.M = (int32_t)M;
+    p.out_bf16 = es == 2 ? 1 : 0;
+    p.xvec = aligned(x, 16) && p.ldx % 8 == 0 && K % 8 == 0 ? 1 : 0;
+    return launch_w4_gemm(p, 256, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+}
+
+gemm355_status gemm355_kv_append(const gemm355_kv_append_args *args, void *stream)
+{
+    KvAppendParams p;
+    const gemm355_status st = append_setup(args, p);
+    if (st != GEMM355_OK || p.c.B == 0 || p.c.tokens == 0) return st;
+    return launch_kv_append(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+}
+
+gemm355_status gemm355_attention_workspace(const gemm355_attention_args *args, size_t *bytes)
+{
+    if (!bytes) return GEMM355_EINVAL;
+    AttnParams p;
+    size_t need = 0;
+    try {
+        const gemm355_status st = attention_setup(args, p, need);
+        if (st != GEMM355_OK) return st;
+    } catch (...) {
+        return GEMM355_ENOMEM;
+    }
+    *bytes = need;
+    return GEMM355_OK;
+}
+
+gemm355_status gemm355_attention(const gemm355_attention_args *args, void *stream)
+{
+    try {
+        AttnParams p;
+        size_t need = 0;
+        gemm355_status st = attention_setup(args, p, need);
+        if (st != GEMM355_OK || p.c.B == 0 || p.c.tokens == 0) return st;
+        void *ws = nullptr;
+        std::unique_lock<std::mutex> hold;
+        if (need && args->workspace) {
+            if (args->workspace_bytes < need) return GEMM355_ENOMEM;
+            if (!aligned(args->workspace, 256)) return GEMM355_EALIGN;
+            ws = args->workspace;
+        } else if (need) {
+            if (capturing(stream)) return GEMM355_ENOMEM;
+            st = library_scratch(need, stream, &ws, hold);
+            if (st != GEMM355_OK) return st;
+        }
+        if (need) {
+            const int64_t slots = (int64_t)p.c.B * p.c.H * p.row_tiles * p.splits;
+            p.part = (float *)ws;
+            p.stat = p.part + slots * 16 * p.D;
+        }
+        return launch_attention(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+    } catch (...) {
+        return GEMM355_ENOMEM;   /* the maps of scratch buffers could not grow */
+    }
+}
 
 gemm355_status gemm355_conv2d(const gemm355_conv_args *args, void *stream)
 {

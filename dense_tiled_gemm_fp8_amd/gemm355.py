@@ -41,6 +41,8 @@ OK, EINVAL, EALIGN, EUNSUPPORTED, ENOMEM, EHIP, ETOOBIG = range(7)
 # 8-bit formats and source types of the quantiser
 FP8_E4M3, FP8_E5M2 = range(2)
 SRC_F32, SRC_BF16 = range(2)
+# formats of a matrix held in 4 bits
+W4_INT, W4_MXFP4 = range(2)
 # layouts
 A_ROW_B_COL, A_ROW_B_ROW, A_COL_B_COL, A_COL_B_ROW = range(4)
 
@@ -97,6 +99,41 @@ class gemm355_conv_args(ctypes.Structure):
     ]
 
 
+class gemm355_w4_matrix(ctypes.Structure):
+    _fields_ = [
+        ("N", _i64), ("K", _i64), ("codes", _vp), ("ldw", _i64), ("scales", _vp), ("zeros", _vp),
+        ("fmt", ctypes.c_int), ("group", _i32),
+    ]
+
+
+class gemm355_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp),
+        ("pages", _i64), ("heads", _i32), ("head_dim", _i32), ("page", _i32),
+        ("batch", _i64), ("table", _vp), ("table_ld", _i64), ("lens", _vp), ("q_start", _vp),
+        ("tokens", _i64), ("max_new", _i64), ("max_len", _i64),
+    ]
+
+
+class gemm355_kv_append_args(ctypes.Structure):
+    _fields_ = [
+        ("cache", gemm355_kv_cache),
+        ("k", _vp), ("ldk", _i64), ("v", _vp), ("ldv", _i64), ("q", _vp), ("ldq", _i64),
+        ("q_out", _vp), ("ldqo", _i64),
+        ("q_heads", _i32), ("rot_dim", _i32), ("interleaved", _i32),
+        ("cos", _vp), ("sin", _vp), ("rot_len", _i64),
+    ]
+
+
+class gemm355_attention_args(ctypes.Structure):
+    _fields_ = [
+        ("cache", gemm355_kv_cache),
+        ("q", _vp), ("ldq", _i64), ("o", _vp), ("ldo", _i64), ("lse", _vp),
+        ("q_heads", _i32), ("scale", ctypes.c_float), ("window", _i64), ("sinks", _i64), ("splits", _i32),
+        ("workspace", _vp), ("workspace_bytes", _sz),
+    ]
+
+
 _lib.gemm355_gemm.restype = ctypes.c_int
 _lib.gemm355_gemm.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                               ctypes.c_int, ctypes.c_int, _i32, _i32, _vp]
@@ -131,6 +168,19 @@ _lib.gemm355_conv2d_out_size.argtypes = [ctypes.POINTER(gemm355_conv_args), ctyp
                                          ctypes.POINTER(_i64)]
 _lib.gemm355_set_scratch_limit.restype = ctypes.c_int
 _lib.gemm355_set_scratch_limit.argtypes = [ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64)]
+_w4p = ctypes.POINTER(gemm355_w4_matrix)
+_lib.gemm355_w4_quantize.restype = ctypes.c_int
+_lib.gemm355_w4_quantize.argtypes = [_vp, _i64, ctypes.c_int, _w4p, _vp]
+_lib.gemm355_w4_dequantize.restype = ctypes.c_int
+_lib.gemm355_w4_dequantize.argtypes = [_w4p, _vp, _i64, ctypes.c_int, _vp]
+_lib.gemm355_w4_gemm.restype = ctypes.c_int
+_lib.gemm355_w4_gemm.argtypes = [_i64, _vp, _i64, _w4p, _vp, _i64, ctypes.c_int, _vp]
+_lib.gemm355_kv_append.restype = ctypes.c_int
+_lib.gemm355_kv_append.argtypes = [ctypes.POINTER(gemm355_kv_append_args), _vp]
+_lib.gemm355_attention.restype = ctypes.c_int
+_lib.gemm355_attention.argtypes = [ctypes.POINTER(gemm355_attention_args), _vp]
+_lib.gemm355_attention_workspace.restype = ctypes.c_int
+_lib.gemm355_attention_workspace.argtypes = [ctypes.POINTER(gemm355_attention_args), ctypes.POINTER(_sz)]
 _lib.gemm355_status_string.restype = ctypes.c_char_p
 _lib.gemm355_status_string.argtypes = [ctypes.c_int]
 
@@ -139,7 +189,8 @@ EXPORTED = ("gemm355_gemm", "gemm355_gemm_ex", "gemm355_gemm_noalloc",
             "gemm355_eta_pad", "gemm355_kslice", "gemm355_unit", "gemm355_num_tiles",
             "gemm355_tile_info", "gemm355_tile_occupancy", "gemm355_quantize",
             "gemm355_conv2d", "gemm355_conv2d_plan", "gemm355_conv2d_out_size", "gemm355_set_scratch_limit",
-            "gemm355_status_string")
+            "gemm355_w4_quantize", "gemm355_w4_dequantize", "gemm355_w4_gemm", "gemm355_kv_append",
+            "gemm355_attention", "gemm355_attention_workspace", "gemm355_status_string")
 
 
 class Gemm355Error(RuntimeError):
@@ -296,3 +347,63 @@ def gemm355_quantize(x, n, batch, src, fmt, q, scale, stream=None) -> None:
     dequantisation factors into scale[batch] (device pointers or tensors)."""
     _check(_lib.gemm355_quantize(_ptr(x), n, batch, src, fmt, _ptr(q), _ptr(scale), _stream(stream)),
            "gemm355_quantize")
+
+
+def make_w4_matrix(N, K, codes=None, scales=None, zeros=None, fmt=W4_INT, group=128, ldw=0) -> gemm355_w4_matrix:
+    """Descriptor of an N x K matrix in 4 bits; it holds addresses, so the
+    tensors must outlive it.  ldw = 0: rows of K rounded up to 32 codes."""
+    return gemm355_w4_matrix(N, K, _ptr(codes), ldw, _ptr(scales), _ptr(zeros), fmt, group)
+
+
+def gemm355_w4_quantize(w, matrix: gemm355_w4_matrix, src=SRC_BF16, ld=0, stream=None) -> None:
+    """Codes, scales and zero points (if any) of `matrix` from the rows of w."""
+    _check(_lib.gemm355_w4_quantize(_ptr(w), ld, src, ctypes.byref(matrix), _stream(stream)), "gemm355_w4_quantize")
+
+
+def gemm355_w4_dequantize(matrix: gemm355_w4_matrix, w, dst=SRC_BF16, ld=0, stream=None) -> None:
+    """The values that `matrix` stands for, into the rows of w."""
+    _check(_lib.gemm355_w4_dequantize(ctypes.byref(matrix), _ptr(w), ld, dst, _stream(stream)),
+           "gemm355_w4_dequantize")
+
+
+def gemm355_w4_gemm(M, x, matrix: gemm355_w4_matrix, y, out=SRC_BF16, ldx=0, ldy=0, stream=None) -> None:
+    """y (M x N, type `out`) = x (M x K, bf16) times the transpose of `matrix`."""
+    _check(_lib.gemm355_w4_gemm(M, _ptr(x), ldx, ctypes.byref(matrix), _ptr(y), ldy, out, _stream(stream)),
+           "gemm355_w4_gemm")
+
+
+def make_kv_cache(k=None, v=None, k_scale=None, v_scale=None, pages=0, heads=0, head_dim=0, page=0, table=None,
+                  lens=None, batch=0, max_len=0, q_start=None, tokens=0, max_new=1, table_ld=0) -> gemm355_kv_cache:
+    """Descriptor of a paged cache and one step on it (addresses only)."""
+    return gemm355_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, heads, head_dim, page, batch,
+                            _ptr(table), table_ld, _ptr(lens), _ptr(q_start), tokens, max_new, max_len)
+
+
+def make_kv_append_args(cache: gemm355_kv_cache, k=None, v=None, q=None, q_out=None, q_heads=0, cos=None, sin=None,
+                        rot_dim=0, rot_len=0, interleaved=False, ldk=0, ldv=0, ldq=0,
+                        ldqo=0) -> gemm355_kv_append_args:
+    return gemm355_kv_append_args(cache, _ptr(k), ldk, _ptr(v), ldv, _ptr(q), ldq, _ptr(q_out), ldqo, q_heads,
+                                  rot_dim, 1 if interleaved else 0, _ptr(cos), _ptr(sin), rot_len)
+
+
+def gemm355_kv_append(args: gemm355_kv_append_args, stream=None) -> None:
+    """The step's keys (rotated) and values into the cache, and the rotated queries."""
+    _check(_lib.gemm355_kv_append(ctypes.byref(args), _stream(stream)), "gemm355_kv_append")
+
+
+def make_attention_args(cache: gemm355_kv_cache, q=None, o=None, q_heads=0, lse=None, scale=0.0, window=0, sinks=0,
+                        splits=0, ldq=0, ldo=0, workspace=None, workspace_bytes=0) -> gemm355_attention_args:
+    return gemm355_attention_args(cache, _ptr(q), ldq, _ptr(o), ldo, _ptr(lse), q_heads, scale, window, sinks, splits,
+                                  _ptr(workspace), workspace_bytes)
+
+
+def gemm355_attention(args: gemm355_attention_args, stream=None) -> None:
+    """Attention of the step's queries over the cache."""
+    _check(_lib.gemm355_attention(ctypes.byref(args), _stream(stream)), "gemm355_attention")
+
+
+def gemm355_attention_workspace(args: gemm355_attention_args) -> int:
+    """Scratch bytes of that call (0: none)."""
+    n = _sz()
+    _check(_lib.gemm355_attention_workspace(ctypes.byref(args), ctypes.byref(n)), "gemm355_attention_workspace")
+    return n.value

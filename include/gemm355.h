@@ -318,7 +318,7 @@ GEMM355_API gemm355_status gemm355_plan(const gemm355_args *args, gemm355_plan_t
  * wave efficiency": split-K's partial sums go to a buffer of their own,
  * combined by a second pass; repacked rows and regrouped block scales use
  * the same buffer).  A call of gemm355_gemm, gemm355_gemm_ex without a
- * workspace, gemm355_conv2d or gemm355_quantize whose plan needs more than
+ * workspace, gemm355_conv2d, gemm355_quantize or gemm355_attention that needs more than
  * `bytes` returns ENOMEM before anything is launched, and a buffer is
  * never grown past the cap; buffers already larger are kept until unload.
  * Calls with a caller workspace and gemm355_gemm_noalloc are not affected.
@@ -501,6 +501,229 @@ GEMM355_API gemm355_status gemm355_conv2d_plan(const gemm355_conv_args *args, ge
  * shape arguments exactly as gemm355_conv2d reports them, EINVAL for NULL
  * pointers. */
 GEMM355_API gemm355_status gemm355_conv2d_out_size(const gemm355_conv_args *args, int64_t *P, int64_t *Q);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Serving operators: what a step of one or a few tokens runs beside the tiled
+ * product.  Weights are held in 4 bits and multiplied by bf16 rows; keys and
+ * values are held in 8 bits in pages and read by attention, the other
+ * workload that page "The Tensor Core" names as reducing to matrix products.
+ * In the arguments below a leading dimension of 0 means packed.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Formats of a matrix held in 4 bits. */
+typedef enum gemm355_w4fmt {
+    GEMM355_W4_INT = 0,     /* codes u = 0 .. 15; the value is (u - z) * s with
+                               a bf16 scale s and a zero point z for each group
+                               of consecutive K-values of a row               */
+    GEMM355_W4_MXFP4 = 1    /* E2M1 codes with one E8M0 scale per 32 K-values:
+                               the elements, packing and scales that
+                               GEMM355_MXFP4_* products take for B; byte 255
+                               makes its block NaN, and values of 2^128 or
+                               more (bytes 253 and 254) are infinities        */
+} gemm355_w4fmt;
+
+/* An N x K matrix W held in 4 bits, row n being output n of a product.  Two
+ * codes a byte, element 2i in the low nibble of byte i of its row. */
+typedef struct gemm355_w4_matrix {
+    int64_t N, K;           /* any sizes >= 0                                 */
+    uint8_t *codes;         /* device, 16-byte aligned (EALIGN); what a row
+                               holds past K does not matter                   */
+    int64_t ldw;            /* elements between rows: a multiple of 32, at
+                               least K (EINVAL); 0: K rounded up to 32        */
+    void *scales;           /* device, dense [N][ceil(K / group)]: bf16 (INT,
+                               2-byte aligned) or E8M0 bytes (MXFP4)          */
+    uint8_t *zeros;         /* INT: device bytes, same shape as scales, or NULL
+                               (every zero point is 8); MXFP4: NULL           */
+    gemm355_w4fmt fmt;
+    int32_t group;          /* K-values with one scale: 32, 64 or 128 (INT),
+                               32 (MXFP4); the last of a row may be short     */
+} gemm355_w4_matrix;
+
+/*
+ * gemm355_w4_quantize -- puts a matrix into 4 bits (the group-wise relative of
+ * gemm355_quantize; section "Practical shape sweep" of page "10. Tensor
+ * Cores, ..." counts quantisation with the product).  For each group of a row:
+ *   INT without zeros:  a = max |w|, s = bf16(a / 7), z = 8
+ *   INT with zeros:     lo = min(0, min w), hi = max(0, max w), a = hi - lo,
+ *                       s = bf16(a / 15), z = clamp(rne(-lo / s), 0, 15)
+ *       u = clamp(rne(w / s) + z, 0, 15); s = 1 where a < 2^-100
+ *   MXFP4:  byte = floor(log2 max |w|) - 2 + 127, at least 0 (0 where all are
+ *           zero); u = the E2M1 code nearest to w / 2^(byte - 127), ties to
+ *           the even code, magnitudes above 6 to 6
+ * with differences and quotients rounded to nearest in fp32, bf16() and rne()
+ * to nearest with ties to even.
+ *   w: device, row n at w + n * ld, K elements of `src`, finite; ld >= K.
+ *   q->codes, q->scales, q->zeros are written (the codes of a row up to K
+ *   rounded up to 8, zeros past K).
+ * One kernel, no scratch.  N or K = 0: nothing is done.
+ * Errors: EINVAL (sizes, enums, null pointers, w overlapping what is written),
+ * EALIGN, EUNSUPPORTED (N or K above 2^30, N * K above 2^40), EHIP.
+ */
+GEMM355_API gemm355_status gemm355_w4_quantize(const void *w, int64_t ld, gemm355_src src,
+                                   const gemm355_w4_matrix *q, void *stream);
+
+/*
+ * gemm355_w4_dequantize -- the values a matrix in 4 bits stands for, rounded
+ * to nearest even once, as fp32 or bf16 rows w + n * ld (for the dense product
+ * gemm355_gemm, whose B column-major this is with ldb = ld, where M is large;
+ * page "10. Tensor Cores, ...", section "Practical shape sweep").
+ * Errors as gemm355_w4_quantize.
+ */
+GEMM355_API gemm355_status gemm355_w4_dequantize(const gemm355_w4_matrix *q, void *w, int64_t ld,
+                                     gemm355_src dst, void *stream);
+
+/*
+ * gemm355_w4_gemm -- y[m][n] = sum_k x[m][k] W[n][k] for a few bf16 rows x
+ * (the skinny end of page "10. Tensor Cores, ...", section "Shape the
+ * operation": M of one token or a decode batch, where the stream of weights
+ * bounds the time).  Any M >= 0 is right; the work is laid out for M up to 64,
+ * beyond that W is read again for every 64 rows and the dense product over
+ * dequantised weights is the faster way.
+ *   x: device bf16, row m at x + m * ldx, ldx >= K, finite.
+ *   y: device, row m at y + m * ldy, ldy >= N, fp32 or bf16 (`out`).
+ * Sums are fp32; scales multiply the sum of a group (INT) or the element,
+ * exactly (MXFP4): weights are never rounded.  One kernel, no scratch, and the
+ * same bits from the same arguments every time.  M or N = 0: nothing is done;
+ * K = 0: y = 0.
+ * Errors: EINVAL (sizes, leading dimensions, enums, null pointers, y
+ * overlapping an input), EALIGN, EUNSUPPORTED (N or K above 2^30, M above
+ * 2^19), EHIP.
+ */
+GEMM355_API gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx,
+                               const gemm355_w4_matrix *w, void *y, int64_t ldy,
+                               gemm355_src out, void *stream);
+
+/*
+ * Keys and values of a batch of sequences in pages of E4M3 codes, with one
+ * E8M0 scale 2^(byte - 127) for each page and head (block scaling as in the
+ * MX dtypes, the block being a page's tokens of one head), and the step that
+ * runs on it.  Sequence b holds lens[b] tokens, the step's new ones included;
+ * its token t is slot t % page of page table[b][t / page].  Its new tokens are
+ * rows q_start[b] .. q_start[b + 1] - 1 of the step's tensors and the last of
+ * the sequence: row q_start[b] + i has position
+ * lens[b] - (q_start[b + 1] - q_start[b]) + i.
+ *
+ * Device contents that host checks cannot see are bounded by the kernels:
+ * lens outside [0, max_len] and q_start outside [0, tokens] or descending are
+ * read as the nearest value allowed, rows past max_new in a sequence are left
+ * out, and tokens whose page id is not in [0, pages) are neither written nor
+ * seen by any row.  Two sequences may share pages that they only read; a page
+ * that a step appends to must belong to one sequence of that step, once.
+ */
+typedef struct gemm355_kv_cache {
+    uint8_t *k;             /* E4M3 [pages][heads][page][head_dim]            */
+    uint8_t *v;             /* E4M3 [pages][heads][head_dim][page]; both
+                               16-byte aligned (EALIGN)                       */
+    uint8_t *k_scale;       /* E8M0 [pages][heads]                            */
+    uint8_t *v_scale;
+    int64_t pages;          /* >= 1                                           */
+    int32_t heads;          /* key heads, >= 1                                */
+    int32_t head_dim;       /* 64, 128 or 256 (EUNSUPPORTED otherwise)        */
+    int32_t page;           /* tokens a page: 16, 32, 64 or 128 (EUNSUPPORTED
+                               otherwise)                                     */
+    int64_t batch;          /* sequences, >= 0                                */
+    const int32_t *table;   /* [batch][table_ld] page ids; entries past a
+                               sequence's last page are not read              */
+    int64_t table_ld;       /* 0: max_len / page, rounded up                  */
+    const int32_t *lens;    /* [batch]                                        */
+    const int32_t *q_start; /* [batch + 1], or NULL: max_new rows a sequence
+                               (tokens = batch * max_new, EINVAL otherwise)   */
+    int64_t tokens;         /* rows of the step's tensors; those behind
+                               q_start[batch] are neither read nor written    */
+    int64_t max_new;        /* most new tokens of a sequence, >= 1            */
+    int64_t max_len;        /* most tokens of a sequence; at most
+                               table_ld * page (EINVAL)                       */
+} gemm355_kv_cache;
+
+/*
+ * gemm355_kv_append -- writes a step's keys and values into the cache, keys
+ * rotated by their position, and the rotated queries.
+ *   Rotation, for pairs (a, b) of the first rot_dim channels of a head and the
+ *   tables' row of the token's position: (a cos - b sin, b cos + a sin).  Pair
+ *   i is channels (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved; other
+ *   channels stay.  Computed in 64 bits, rounded to fp32, then to the output.
+ *   Scale of a page and head: e is the smallest exponent with
+ *   max |new| <= 448 * 2^e, at least -100 and at most 120.  Where the page
+ *   begins with a new token its scale becomes 2^e; else it becomes the larger
+ *   of the old one and 2^e, and if it grew, the codes of the older tokens are
+ *   rewritten as the nearest codes of their old values.  Codes are nearest,
+ *   ties to even.  The slots behind a sequence's last token stay as they were.
+ *   k, v: device bf16, row r head h at k + r * ldk + h * head_dim; finite (an
+ *   infinity is held as the largest value, a NaN as a NaN).
+ *   q, q_out: the same with q_heads heads, or both NULL; q_out gets bf16 rows
+ *   (not those of tokens at negative positions).
+ * All rows 16-byte aligned: pointers (EALIGN), ld* multiples of 8 (EINVAL).
+ * One kernel, no scratch.
+ * Errors: EINVAL (sizes, null pointers, q_out overlapping an input, the cache
+ * overlapping one, rot_len < max_len), EALIGN, EUNSUPPORTED, EHIP.
+ */
+typedef struct gemm355_kv_append_args {
+    gemm355_kv_cache cache;
+    const void *k;  int64_t ldk;
+    const void *v;  int64_t ldv;
+    const void *q;  int64_t ldq;
+    void *q_out;    int64_t ldqo;
+    int32_t q_heads;
+    int32_t rot_dim;        /* even, 0 (no rotation) .. head_dim              */
+    int32_t interleaved;
+    const float *cos, *sin; /* device fp32 [rot_len][rot_dim / 2]             */
+    int64_t rot_len;        /* positions the tables hold, >= max_len          */
+} gemm355_kv_append_args;
+
+GEMM355_API gemm355_status gemm355_kv_append(const gemm355_kv_append_args *args, void *stream);
+
+/*
+ * gemm355_attention -- attention of the step's queries over the cache (page
+ * "The Tensor Core": attention reduces to matrix products).  The row of token
+ * position p and query head j reads key head j / (q_heads / heads) and sees
+ * the tokens t <= p of its sequence with t > p - window or t < sinks (window
+ * 0: all of them):
+ *     o = sum_t softmax_t(scale * q . k_t) v_t,  lse = log sum_t exp(scale * q . k_t).
+ * A row that sees nothing gets o = 0 and lse = -infinity.  What a row does not
+ * see has no effect on it, whatever it holds; a NaN in a value that a row sees
+ * makes that row NaN, in that channel at least.
+ *   q, o: device bf16, row r head j at q + r * ldq + j * head_dim, rows 16-byte
+ *   aligned (pointers EALIGN, ld* multiples of 8 EINVAL); o is written.
+ *   lse: device fp32 [tokens][q_heads], written, or NULL.
+ * Products and statistics are fp32; the softmax weights enter the second
+ * product as bf16.
+ * The key axis is split into `splits` parts where there are few rows (0:
+ * chosen from the sizes; at most one part per 256 tokens); parts go through
+ * scratch and a second kernel, in a fixed order, so the same arguments give
+ * the same bits.  Scratch is the caller's workspace (256-byte aligned, EALIGN;
+ * at least gemm355_attention_workspace bytes, ENOMEM) or library-owned (capped
+ * by gemm355_set_scratch_limit).  A stream that is being captured needs a
+ * workspace of its own where scratch is needed (ENOMEM otherwise): a graph's
+ * replays would use library-owned memory that later calls may move.
+ * Errors: EINVAL (sizes, null pointers, o or lse overlapping an input or each
+ * other, a scale that is negative or not finite), EALIGN, EUNSUPPORTED, ENOMEM,
+ * EHIP.
+ */
+typedef struct gemm355_attention_args {
+    gemm355_kv_cache cache;
+    const void *q;  int64_t ldq;
+    void *o;        int64_t ldo;
+    float *lse;
+    int32_t q_heads;        /* a multiple of cache.heads                      */
+    float scale;            /* 0: 1 / sqrt(head_dim)                          */
+    int64_t window, sinks;  /* >= 0                                           */
+    int32_t splits;
+    void *workspace;
+    size_t workspace_bytes;
+} gemm355_attention_args;
+
+GEMM355_API gemm355_status gemm355_attention(const gemm355_attention_args *args, void *stream);
+
+/* Scratch of that call in bytes (0 where the key axis is not split), to *bytes,
+ * a host pointer.  Host arithmetic over the sizes and the current device's
+ * compute units (256 without a device); pointers are checked as by
+ * gemm355_attention, never read.  The partial sums of a split key axis are
+ * the counterpart of split-K's (page "10. Tensor Cores, ...", section "When
+ * shape alone can't fix wave efficiency").  Errors: those of
+ * gemm355_attention, EINVAL for a NULL bytes. */
+GEMM355_API gemm355_status gemm355_attention_workspace(const gemm355_attention_args *args, size_t *bytes);
 
 /* Static description of a status code (this library's own codes; no
  * passage of the pages defines them).  Never NULL: unknown codes get a

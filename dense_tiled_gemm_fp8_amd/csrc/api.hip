@@ -477,6 +477,7 @@ gemm355_status conv_setup(const gemm355_conv_args *c, gemm355_args &a, ConvShape
 /* ---- serving operators: argument checks ---- */
 
 const int64_t kMaxDim = (int64_t)1 << 30;
+const int64_t kMaxWide = (int64_t)1 << 24;
 
 /* Extent in bytes of `rows` rows of `cols` elements, ld elements apart. */
 struct Span {
@@ -679,12 +680,14 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     p.window = a->window >= c.max_len ? 0 : (int32_t)a->window;
     p.sinks = (int32_t)std::min<int64_t>(a->sinks, c.max_len);
     const int64_t rows = (int64_t)p.c.max_new * p.group;
+    p.tile_rows = rows <= 16 ? 16 : rows <= 32 || p.D == 256 ? 32 : 64;
     if (rows > (int64_t)16 * 65535) return GEMM355_EUNSUPPORTED;
-    p.row_tiles = (int32_t)((rows + 15) / 16);
+    p.row_tiles = (int32_t)((rows + p.tile_rows - 1) / p.tile_rows);
     const int64_t tiles = std::max<int64_t>(1, c.batch * c.heads * p.row_tiles);
     int64_t seen = c.max_len;
     if (p.window) seen = std::min(seen, (int64_t)p.window + p.c.max_new + p.sinks + 128);
-    const int64_t most = std::max<int64_t>(1, (seen + 255) / 256);
+    p.part_chunks = a->splits ? 4 : 24;
+    const int64_t most = std::max<int64_t>(1, (seen + 64 * p.part_chunks - 1) / (64 * p.part_chunks));
     const int32_t cus = [] {
         int n = 0;
         if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
@@ -696,7 +699,7 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     const int64_t want = a->splits ? a->splits : (2 * (int64_t)cus + tiles - 1) / tiles;
     p.splits = (int32_t)std::min(want, most);
     const int64_t slots = tiles * p.splits;
-    bytes = p.splits > 1 ? (size_t)slots * 16 * (size_t)(p.D + 2) * sizeof(float) : 0;
+    bytes = p.splits > 1 ? (size_t)slots * (size_t)p.tile_rows * (size_t)(p.D + 2) * sizeof(float) : 0;
     p.part = p.stat = nullptr;
     return GEMM355_OK;
 }
@@ -745,7 +748,8 @@ gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx, const gemm
     p.ldx = ldx ? ldx : K;
     p.ldy = ldy ? ldy : N;
     if (p.ldx < K || p.ldy < N) return GEMM355_EINVAL;
-    if (p.ldx > kMaxDim || p.ldy > kMaxDim) return GEMM355_EUNSUPPORTED;
+    /* the kernel's 32-bit offsets span 64 rows */
+    if (p.ldx > kMaxWide || p.w.ldb > kMaxWide / 2 || p.ldy > kMaxDim) return GEMM355_EUNSUPPORTED;
     if (M > 0 && N > 0 && (!y || (K > 0 && !x))) return GEMM355_EINVAL;
     if (!aligned(x, 2) || !aligned(y, (uintptr_t)es)) return GEMM355_EALIGN;
     const Span ys(y, M, N, p.ldy, es);
@@ -758,8 +762,13 @@ gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx, const gemm
     p.y = y;
     p.M = (int32_t)M;
     p.out_bf16 = es == 2 ? 1 : 0;
-    p.xvec = aligned(x, 16) && p.ldx % 8 == 0 && K % 8 == 0 ? 1 : 0;
-    return launch_w4_gemm(p, 256, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+    /* scales and zero points are read by whole dwords */
+    const int64_t groups = N * p.w.ng;
+    p.even = aligned(x, 16) && p.ldx % 8 == 0 && K % 128 == 0 && aligned(w->scales, 4) && aligned(w->zeros, 4) &&
+                     groups % (p.w.zeros ? 4 : p.w.mx ? 1 : 2) == 0
+                 ? 1
+                 : 0;
+    return launch_w4_gemm(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
 }
 
 gemm355_status gemm355_kv_append(const gemm355_kv_append_args *args, void *stream)
@@ -806,7 +815,7 @@ gemm355_status gemm355_attention(const gemm355_attention_args *args, void *strea
         if (need) {
             const int64_t slots = (int64_t)p.c.B * p.c.H * p.row_tiles * p.splits;
             p.part = (float *)ws;
-            p.stat = p.part + slots * 16 * p.D;
+            p.stat = p.part + slots * p.tile_rows * p.D;
         }
         return launch_attention(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
     } catch (...) {

@@ -28,6 +28,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "dma.h"
 #include "kernels.h"
 #include "sched.h"
 #include "tiles.h"
@@ -39,14 +40,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void_t;
-
-/* Buffer loads whose offset is past num_records return zero (and write zero
- * to LDS for the direct-to-LDS form): rows beyond M or N and K-chunks beyond
- * K are read through offset kOOB. */
-constexpr uint32_t kNumRecords = 0x7FFFFF00u;
-constexpr uint32_t kOOB = 0x80000000u;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base)
 {
@@ -55,70 +49,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base)
                                              0x00020000);
 }
 
-/* The four dwords of a raw buffer resource: 48-bit base, stride 0,
- * num_records, and the gfx9-family word 3 (32-bit data format). */
-__device__ __forceinline__ i32x4 rsrc_words(const void *base)
-{
-    const uint64_t a = (uint64_t)(uintptr_t)base;
-    return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
-                 __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xFFFF),
-                 (int)kNumRecords, 0x00020000};
-}
-
 /* The lane's index in its wavefront, counted from the execution mask
  * (every lane active): needs no register held since the kernel's start. */
 __device__ __forceinline__ int lane_id()
 {
     return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
-}
-
-/* 32-bit LDS address of a __shared__ object. */
-__device__ __forceinline__ uint32_t lds_addr(const uint8_t *p)
-{
-    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)p;
-}
-
-/* Compile-time unrolling: f(integral_constant<int, t>) for t = 0 .. N-1. */
-template <int... T, class F>
-__device__ __forceinline__ void unroll_seq(std::integer_sequence<int, T...>, F &&f)
-{
-    (f(std::integral_constant<int, T>{}), ...);
-}
-template <int N, class F>
-__device__ __forceinline__ void unroll(F &&f)
-{
-    unroll_seq(std::make_integer_sequence<int, N>{}, static_cast<F &&>(f));
-}
-
-/* One direct-to-LDS copy: each lane fetches 16 bytes at voffset from the
- * buffer and the wavefront writes them to LDS at lds_base + OFF .. + 1023
- * (lane l at + 16 l).  Issued as inline assembly so that the compiler neither
- * waits for it before unrelated LDS reads nor counts it (completion is
- * awaited explicitly), and so that the LDS address is formed in M0 right at
- * the load from one base register and an immediate. */
-template <int OFF>
-__device__ __forceinline__ void dma16(const i32x4 &rsrc, uint32_t lds_base, uint32_t voffset)
-{
-    /* s_add writes SCC: declared clobbered, or the compiler could keep a
-     * comparison result in SCC across this statement */
-    int m0_out;
-    asm volatile("s_add_u32 m0, %2, %4\n\tbuffer_load_dwordx4 %1, %3, 0 offen lds"
-                 : "={m0}"(m0_out)
-                 : "v"(voffset), "s"(lds_base), "s"(rsrc), "n"(OFF)
-                 : "memory", "scc");
-    (void)m0_out;
-}
-
-/* One direct-to-LDS dword copy: lane l fetches 4 bytes at voffset and the
- * wavefront writes them to LDS at lds_addr + 4 l (256 bytes). */
-__device__ __forceinline__ void dma4(const i32x4 &rsrc, uint32_t lds_addr_, uint32_t voffset)
-{
-    int m0_out;
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %1, %3, 0 offen lds"
-                 : "={m0}"(m0_out)
-                 : "v"(voffset), "s"(lds_addr_), "s"(rsrc)
-                 : "memory");
-    (void)m0_out;
 }
 
 /* All of this wave's direct-to-LDS copies have landed, then the workgroup
@@ -131,14 +66,6 @@ __device__ __forceinline__ void stage_barrier()
     asm volatile("" ::: "memory");
 }
 
-/* Wait until at most N vector-memory operations of this wave are
- * outstanding (loads complete in issue order). */
-template <int N>
-__device__ __forceinline__ void wait_vmcnt()
-{
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
 
 template <int V> using IC = std::integral_constant<int, V>;
 

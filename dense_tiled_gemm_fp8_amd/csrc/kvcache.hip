@@ -19,6 +19,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "dma.h"
 #include "serve.h"
 
 namespace g355 {
@@ -29,6 +30,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float bf16_value(uint32_t h) { return __builtin_bit_cast(float, h << 16); }
 
@@ -281,9 +283,9 @@ hipError_t launch_kv_append(const KvAppendParams &p, hipStream_t stream)
 
 namespace {
 
-/* What a tile of rows sees: rows r0 .. r0 + 15 of a sequence's n * group, the
- * positions of the first and last, and the 64-token chunks to visit (those of
- * the first tokens that stay visible, then the run that ends at the last
+/* What a tile of rows sees: `count` rows from r0 on of a sequence's n * group,
+ * the positions of the first and last, and the 64-token chunks to visit (those
+ * of the first tokens that stay visible, then the run that ends at the last
  * row's position). */
 struct Tile {
     Seq s;
@@ -292,15 +294,13 @@ struct Tile {
     int32_t parts;                /* splits with work                         */
 };
 
-constexpr int kAttnWaves = 4;
-
-__device__ __forceinline__ Tile row_tile(const AttnParams &p, int32_t b, int32_t r0)
+__device__ __forceinline__ Tile row_tile(const AttnParams &p, int32_t b, int32_t r0, int32_t count)
 {
     Tile t;
     t.s = sequence(p.c, b);
     t.rows = t.s.n * p.group;
     t.pos_lo = t.s.pos + r0 / p.group;
-    t.pos_hi = t.s.pos + min(r0 + 15, t.rows - 1) / p.group;
+    t.pos_hi = t.s.pos + min(r0 + count - 1, t.rows - 1) / p.group;
     t.sink_chunks = t.first_chunk = t.total = 0;
     if (r0 < t.rows && t.pos_hi >= 0) {
         if (p.window) {
@@ -309,7 +309,7 @@ __device__ __forceinline__ Tile row_tile(const AttnParams &p, int32_t b, int32_t
         }
         t.total = t.sink_chunks + ((t.pos_hi + 64) >> 6) - t.first_chunk;
     }
-    t.parts = min(p.splits, max((t.total + kAttnWaves - 1) / kAttnWaves, 1));
+    t.parts = min(p.splits, max((t.total + p.part_chunks - 1) / p.part_chunks, 1));
     return t;
 }
 
@@ -324,9 +324,8 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t a, uint32_t b, float s)
     return __builtin_bit_cast(bf16x8, v);
 }
 
-/* Output row of a tile's row r: bf16 sums over the total weight, and the
- * logarithm of that weight. */
-template <int D>
+/* Four channels of a row r: bf16 sums over the total weight, and the logarithm
+ * of that weight. */
 __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, int32_t h, int32_t r, int32_t dt, int32_t q, f32x4 sum,
                                           float m, float l)
 {
@@ -334,7 +333,7 @@ __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, in
     const int64_t row = t.s.row + i;
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     const float a = sum[0] * inv, b = sum[1] * inv, c = sum[2] * inv, d = sum[3] * inv;
-    *(uint2 *)(p.o + row * p.ldo + head * D + 16 * dt + 4 * q) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+    *(uint2 *)(p.o + row * p.ldo + head * p.D + 16 * dt + 4 * q) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
     if (p.lse && dt == 0 && q == 0)
         p.lse[row * p.Hq + head] = l > 0.0f || l != l ? (m + __builtin_log2f(l)) * 0.69314718055994531f : -__builtin_inff();
 }
@@ -342,255 +341,465 @@ __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, in
 } /* namespace */
 
 /*
- * A workgroup: 16 rows of one sequence and key head, one part of their
- * chunks; its wavefronts take the chunks (64 tokens) in turn, each with its
+ * A workgroup: 16 NR rows of one sequence and key head, one part of their
+ * chunks; its NW wavefronts take the chunks (64 tokens) in turn, each with its
  * own running maximum and sum, and join in LDS at the end.
  *
  * Both products run on v_mfma_f32_16x16x32_bf16 with the cache as the first
- * operand: S^T = K Q^T, O^T = V^T P^T.  Lane l is row r = l % 16 of the tile
- * in both results and in P^T, so softmax statistics are one value a lane.
- * The matrix instruction sums over any order of its 32 values that both
+ * operand: S^T = K Q^T, O^T = V^T P^T.  Lane l is row l % 16 of a row tile in
+ * both results and in P^T, so softmax statistics are one value a lane and row
+ * tile.  The matrix instruction sums over any order of its 32 values that both
  * operands share, and takes its rows in any order; so product t of a chunk
  * takes as row i = 4a + b the token 16a + 4t + b.  Lane (r, q) then gets the
  * scores of tokens 16q .. 16q + 15, which is the order in which it holds P^T
- * for the second product and loads 16 contiguous tokens of a channel of V:
- * nothing is exchanged between lanes.  A lane's D / 4 channels of a key row are
- * contiguous as well.  Codes become bf16 with the block's power of two
- * in one conversion, exactly.
+ * for the second product and takes 16 contiguous tokens of a channel of V:
+ * nothing is exchanged between lanes.  Codes become bf16 with the block's power
+ * of two in one conversion, exactly.
+ *
+ * The cache goes straight to LDS, lanes along a token's channels (K) or a
+ * channel's tokens (V) so that the memory unit gets its 64 bytes from four
+ * neighbours; loads in the matrix order took four times the cycles.  Units of
+ * 16 bytes are exchanged within a token's (a channel's) row, so that the
+ * reads are free of bank conflicts.  A wavefront has room for one chunk of each:
+ * the next chunk's keys are sent off when this one's are read, under the softmax
+ * and the second product, its values when that product has read its own; page
+ * ids come one chunk further ahead and scales with their pages, all by the same
+ * copies, so the waits below count them all and the compiler adds none.
  */
-template <int D>
-__global__ __launch_bounds__(kAttnWaves * 64) void attention_kernel(AttnParams p)
+template <int D, int NR, int NW>
+__global__ __launch_bounds__(NW * 64) void attention_kernel(AttnParams p)
 {
-    constexpr int DT = D / 16, DS = D / 32, DL = D / 64;
+    constexpr int DT = D / 16, DS = D / 32, DL = D / 64, UNITS = D / 16;
+    constexpr bool QLDS = NR > 2;                  /* queries in LDS           */
     const KvParams &c = p.c;
-    const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t lr = lane & 15, q = lane >> 4;
-    const int32_t b = blockIdx.z / c.H, h = blockIdx.z % c.H, r0 = blockIdx.y * 16;
-    const Tile t = row_tile(p, b, r0);
+    const int32_t b = blockIdx.z / c.H, h = blockIdx.z % c.H, r0 = blockIdx.y * (16 * NR);
+    const Tile t = row_tile(p, b, r0, 16 * NR);
     if (r0 >= t.rows || (int32_t)blockIdx.x >= t.parts) return;
     const int32_t begin = (int32_t)((int64_t)t.total * blockIdx.x / t.parts);
     const int32_t end = (int32_t)((int64_t)t.total * (blockIdx.x + 1) / t.parts);
 
-    const int32_t r = min(r0 + lr, t.rows - 1);
-    const int32_t pos = t.s.pos + r / p.group;
-    const uint16_t *qrow = p.q + (int64_t)(t.s.row + r / p.group) * p.ldq + (h * p.group + r % p.group) * D + q * (D / 4);
-    bf16x8 qf[DS];
-#pragma unroll
-    for (int i = 0; i < DS; ++i) qf[i] = __builtin_bit_cast(bf16x8, *(const uint4 *)(qrow + 8 * i));
+    /* LDS of a wavefront: a chunk of keys, one of values, page ids of two
+     * chunks, scales of a chunk's key and value pages; behind the loop the
+     * sums to join */
+    constexpr int KB = 64 * D, OWN = 2 * KB + 4 * 256;
+    constexpr int JOIN = NW / 2 * NR * DT * 1024;
+    __shared__ __align__(16) uint8_t store[NW * OWN > JOIN ? NW * OWN : JOIN];
+    __shared__ u32x4 queries[QLDS ? NR * DS * 64 : 1];
+    __shared__ float st[NW][2][16 * NR];
+    const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(store) + wave * OWN);
+    uint8_t *own = store + wave * OWN;
 
-    f32x4 o[DT];
+    int32_t pos[NR];
+    bf16x8 qf[QLDS ? 1 : NR][DS];
 #pragma unroll
-    for (int i = 0; i < DT; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -__builtin_inff(), l = 0.0f;
-    const int32_t ksub = lr >> 2;                 /* 16-token block of the lane's key rows */
+    for (int i = 0; i < NR; ++i) {
+        const int32_t r = min(r0 + 16 * i + lr, t.rows - 1);
+        pos[i] = t.s.pos + r / p.group;
+        const uint16_t *row = p.q + (int64_t)(t.s.row + r / p.group) * p.ldq + (h * p.group + r % p.group) * D + q * (D / 4);
+        if constexpr (QLDS) {
+            for (int x = wave; x < DS; x += NW) queries[(i * DS + x) * 64 + lane] = *(const u32x4 *)(row + 8 * x);
+        } else {
+#pragma unroll
+            for (int x = 0; x < DS; ++x) qf[i][x] = __builtin_bit_cast(bf16x8, *(const u32x4 *)(row + 8 * x));
+        }
+    }
+    if constexpr (QLDS) __syncthreads();
+
+    f32x4 o[NR][DT];
+    float m[NR], l[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        m[i] = -__builtin_inff();
+        l[i] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < DT; ++x) o[i][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    /* 16-token blocks: of the chunk's four, the one of the lane's key rows
+     * (ksub), of its scores and values (q), and that its copies of values take
+     * (vsub; lane i < 4 has block i) */
+    const int32_t ksub = lr >> 2, vsub = (lane & 3) ^ q;
     const int32_t *table = c.table + (int64_t)b * c.table_ld;
+    auto token0 = [&](int32_t it) __attribute__((always_inline)) {
+        return (it < t.sink_chunks ? it : t.first_chunk + it - t.sink_chunks) << 6;
+    };
+    /* copies of keys: unit `lane % UNITS` of a row takes the piece that is
+     * exchanged into it, by the token's low bits and its block */
+    const int32_t krow = lane / UNITS;
+    uint32_t key_at[DL];
+#pragma unroll
+    for (int y = 0; y < DL; ++y) {
+        const int32_t tk = y * (64 / UNITS) + krow;
+        const int32_t swap = D == 64 ? 0 : D == 128 ? tk >> 1 & 1 : tk & 3;
+        key_at[y] = (uint32_t)(tk * D + ((lane % UNITS) ^ swap) * 16);
+    }
+    constexpr int BLOCK_BITS = D == 64 ? 4 : D == 128 ? 5 : 6;
 
-    for (int32_t it = begin + wave; it < end; it += kAttnWaves) {
-        const int32_t t0 = (it < t.sink_chunks ? it : t.first_chunk + it - t.sink_chunks) << 6;
-        const int32_t kt = t0 + 16 * ksub, vt = t0 + 16 * q;
-        int32_t kid = -1, vid = -1;
-        if (kt < t.s.len) kid = table[kt >> c.page_log2];
-        if (vt < t.s.len) vid = table[vt >> c.page_log2];
-        const bool kok = kid >= 0 && kid < c.pages, vok = vid >= 0 && vid < c.pages;
-        uint4 kr[4][DL], vr[DT];
-        float ks = 1.0f, vs = 1.0f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int y = 0; y < DL; ++y) kr[x][y] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int x = 0; x < DT; ++x) vr[x] = make_uint4(0, 0, 0, 0);
-        if (kok) {
-            const int64_t block = (int64_t)kid * c.H + h;
-            const uint8_t *at = c.k + (block * c.page + (kt & (c.page - 1)) + (lr & 3)) * D + q * (D / 4);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int y = 0; y < DL; ++y) kr[x][y] = *(const uint4 *)(at + 4 * x * D + 16 * y);
-            ks = __builtin_bit_cast(float, (uint32_t)c.k_scale[block] << 23);
-        }
-        if (vok) {
-            const int64_t block = (int64_t)vid * c.H + h;
-            const uint8_t *at = c.v + (block * D + lr) * c.page + (vt & (c.page - 1));
-#pragma unroll
-            for (int x = 0; x < DT; ++x) vr[x] = *(const uint4 *)(at + 16 * x * c.page);
-            vs = __builtin_bit_cast(float, (uint32_t)c.v_scale[block] << 23);
-        }
-
-        f32x4 s[4];
+    auto copy_ids = [&](int32_t half, int32_t it) __attribute__((always_inline)) {
+        const int32_t tk = min(token0(min(it, end - 1)) + 16 * vsub, t.s.len - 1);
+        dma_global4(base + 2 * KB + half * 256, table + (tk >> c.page_log2));
+    };
+    /* page id of the copies' block, 0 in place of one that is no page (its
+     * tokens are masked); `all` of the lane's blocks are pages of tokens held */
+    auto ids_of = [&](int32_t half, int32_t t0, int32_t &id, bool &kok, bool &vok) __attribute__((always_inline)) {
+        const int32_t *ids = (const int32_t *)(own + 2 * KB + half * 256);
+        const int32_t v = ids[lane], kid = ids[ksub], vid = ids[q];
+        id = v >= 0 && v < c.pages ? v : 0;
+        kok = kid >= 0 && kid < c.pages && t0 + 16 * ksub < t.s.len;
+        vok = vid >= 0 && vid < c.pages && t0 + 16 * q < t.s.len;
+    };
+    auto copy_keys = [&](int32_t id, int32_t t0) __attribute__((always_inline)) {
+        dma_global1(base + 2 * KB + 512, c.k_scale + ((int64_t)id * c.H + h));
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            s[x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            const int64_t block = (int64_t)__builtin_amdgcn_readlane(id, x) * c.H + h;
+            const uint8_t *at = c.k + (block * c.page + ((t0 + 16 * x) & (c.page - 1))) * D;
+#pragma unroll
+            for (int y = 0; y < DL; ++y) dma_global16(base + (x * DL + y) * 1024, at + (key_at[y] ^ (uint32_t)(x << BLOCK_BITS)));
+        }
+    };
+    auto copy_values = [&](int32_t id, int32_t t0) __attribute__((always_inline)) {
+        const int64_t block = (int64_t)id * c.H + h;
+        dma_global1(base + 2 * KB + 768, c.v_scale + block);
+        const uint8_t *at = c.v + (block * D + (lane >> 2)) * c.page + ((t0 + 16 * vsub) & (c.page - 1));
+#pragma unroll
+        for (int x = 0; x < DT; ++x) dma_global16(base + KB + x * 1024, at + 16 * x * c.page);
+    };
+    constexpr int KEYS = 2 + 4 * DL, VALUES = 1 + DT;   /* copies sent together */
+
+    int32_t it = begin + wave;
+    if (it < end) {
+        int32_t t0 = token0(it), id, half = 0;
+        bool kok, vok;
+        copy_ids(0, it);
+        wait_vmcnt<0>();
+        ids_of(0, t0, id, kok, vok);
+        copy_ids(1, it + NW);
+        copy_keys(id, t0);
+        copy_values(id, t0);
+#pragma unroll 1
+        for (; it < end; it += NW) {
+            const int32_t vt = t0 + 16 * q;
+
+            wait_vmcnt<VALUES>();
+            const float ks = __builtin_bit_cast(float, *(const uint32_t *)(own + 2 * KB + 512 + 4 * ksub) << 23);
+            f32x4 s[NR][4];
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) s[i][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int y = 0; y < DL; ++y) {
-                s[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(kr[x][y].x, kr[x][y].y, ks), qf[2 * y], s[x], 0, 0, 0);
-                s[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(kr[x][y].z, kr[x][y].w, ks), qf[2 * y + 1], s[x], 0, 0, 0);
-            }
-        }
-
-        /* every row sees every token of the chunk, or masks */
-        const bool inside = t0 + 63 <= t.pos_lo && (!p.window || t0 > t.pos_hi - p.window || t0 + 63 < p.sinks);
-        if (!inside || __ballot(!vok) != 0) {
-            uint32_t any[4] = {0, 0, 0, 0};       /* bytes of tokens that some row sees */
-            uint32_t mine = 0;                    /* tokens that this row sees          */
+                u32x4 kr[4];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const int32_t tk = vt + x;
-                if (vok && tk <= pos && (!p.window || tk > pos - p.window || tk < p.sinks)) mine |= 1u << x;
-                if (vok && tk <= t.pos_hi && (!p.window || tk > t.pos_lo - p.window || tk < p.sinks)) any[x >> 2] |= 0xFFu << (8 * (x & 3));
-            }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) s[x >> 2][x & 3] = mine >> x & 1u ? s[x >> 2][x & 3] : -__builtin_inff();
-            /* tokens that no row sees may hold anything, a NaN too, which
-             * a weight of zero would not keep out of the sums */
-            uint32_t nan[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int x = 0; x < DT; ++x) {
-                vr[x] = make_uint4(vr[x].x & any[0], vr[x].y & any[1], vr[x].z & any[2], vr[x].w & any[3]);
-                nan[0] |= (vr[x].x & 0x7F7F7F7Fu) + 0x01010101u;
-                nan[1] |= (vr[x].y & 0x7F7F7F7Fu) + 0x01010101u;
-                nan[2] |= (vr[x].z & 0x7F7F7F7Fu) + 0x01010101u;
-                nan[3] |= (vr[x].w & 0x7F7F7F7Fu) + 0x01010101u;
-            }
-            const uint32_t some = (nan[0] | nan[1] | nan[2] | nan[3]) & 0x80808080u;
-            if (__ballot(some != 0) != 0) {
-                /* a NaN that some of the rows see: out of the values, and
-                 * into the scores of those rows */
-                uint32_t tok = 0;
-#pragma unroll
-                for (int x = 0; x < 16; ++x) tok |= (nan[x >> 2] >> (8 * (x & 3) + 7) & 1u) << x;
-                for (int off = 1; off < 16; off <<= 1) tok |= __shfl_xor(tok, off, 64);
-                uint32_t clean[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    if (tok >> x & 1u) {
-                        if (mine >> x & 1u) s[x >> 2][x & 3] = __builtin_nanf("");
-                    } else {
-                        clean[x >> 2] |= 0xFFu << (8 * (x & 3));
-                    }
+                for (int x = 0; x < 4; ++x) {
+                    const int32_t tk = 16 * ksub + 4 * x + (lr & 3);
+                    const int32_t swap = D == 64 ? ksub : D == 128 ? (tk >> 1 & 1) | ksub << 1 : (tk & 3) | ksub << 2;
+                    kr[x] = *(const u32x4 *)(own + tk * D + (((q * DL + y) ^ swap) << 4));
                 }
 #pragma unroll
-                for (int x = 0; x < DT; ++x)
-                    vr[x] = make_uint4(vr[x].x & clean[0], vr[x].y & clean[1], vr[x].z & clean[2], vr[x].w & clean[3]);
+                for (int z = 0; z < 2; ++z) {
+                    bf16x8 kf[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) kf[x] = decode8(kr[x][2 * z], kr[x][2 * z + 1], ks);
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        bf16x8 f;
+                        if constexpr (QLDS)
+                            f = __builtin_bit_cast(bf16x8, queries[(i * DS + 2 * y + z) * 64 + lane]);
+                        else
+                            f = qf[i][2 * y + z];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[i][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[x], f, s[i][x], 0, 0, 0);
+                    }
+                }
             }
-        }
+            /* this chunk's keys are read: the next one's, and ids after that */
+            const int32_t t1 = token0(min(it + NW, end - 1));
+            int32_t id1;
+            bool kok1, vok1;
+            ids_of(half ^ 1, t1, id1, kok1, vok1);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            copy_ids(half, it + 2 * NW);
+            copy_keys(id1, t1);
 
-        float top = -__builtin_inff();
+            /* every row sees every token of the chunk, or masks */
+            const bool inside = t0 + 63 <= t.pos_lo && (!p.window || t0 > t.pos_hi - p.window || t0 + 63 < p.sinks);
+            if (!inside || __ballot(!(kok && vok)) != 0) {
+                uint32_t any[4] = {0, 0, 0, 0};   /* bytes of tokens that some row sees */
+                uint32_t mine[NR];                /* tokens that the lane's rows see    */
 #pragma unroll
-        for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fmaxf(s[x][0], s[x][1]), fmaxf(s[x][2], s[x][3])));
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float now = fmaxf(m, top * p.scale_log2);
-        const float ref = now == -__builtin_inff() ? 0.0f : now;   /* no token seen yet */
-        const float fade = __builtin_amdgcn_exp2f(m - ref);
-        m = now;
-        float sum = 0.0f;
+                for (int i = 0; i < NR; ++i) mine[i] = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+                for (int x = 0; x < 16; ++x) {
+                    const int32_t tk = vt + x;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][y], p.scale_log2, -ref));
-                s[x][y] = e;
-                sum += e;
+                    for (int i = 0; i < NR; ++i)
+                        if (vok && tk <= pos[i] && (!p.window || tk > pos[i] - p.window || tk < p.sinks)) mine[i] |= 1u << x;
+                    if (vok && tk <= t.pos_hi && (!p.window || tk > t.pos_lo - p.window || tk < p.sinks))
+                        any[x >> 2] |= 0xFFu << (8 * (x & 3));
+                }
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) s[i][x >> 2][x & 3] = mine[i] >> x & 1u ? s[i][x >> 2][x & 3] : -__builtin_inff();
+                /* tokens that no row sees may hold anything, a NaN too, which
+                 * a weight of zero would not keep out of the sums: their bytes
+                 * are cleared (a lane clears what it reads itself) */
+                wait_vmcnt<KEYS>();
+                u32x4 *mem = (u32x4 *)(own + KB) + lr * 4 + (q ^ (lr >> 2));
+                uint32_t nan[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int x = 0; x < DT; ++x) {
+                    u32x4 v = mem[x * 64];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        v[y] &= any[y];
+                        nan[y] |= (v[y] & 0x7F7F7F7Fu) + 0x01010101u;
+                    }
+                    mem[x * 64] = v;
+                }
+                const uint32_t some = (nan[0] | nan[1] | nan[2] | nan[3]) & 0x80808080u;
+                if (__ballot(some != 0) != 0) {
+                    /* a NaN that some of the rows see: out of the values, and
+                     * into the scores of those rows */
+                    uint32_t tok = 0;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) tok |= (nan[x >> 2] >> (8 * (x & 3) + 7) & 1u) << x;
+                    for (int off = 1; off < 16; off <<= 1) tok |= __shfl_xor(tok, off, 64);
+                    uint32_t clean[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        if (!(tok >> x & 1u)) clean[x >> 2] |= 0xFFu << (8 * (x & 3));
+#pragma unroll
+                        for (int i = 0; i < NR; ++i)
+                            if ((tok & mine[i]) >> x & 1u) s[i][x >> 2][x & 3] = __builtin_nanf("");
+                    }
+#pragma unroll
+                    for (int x = 0; x < DT; ++x) {
+                        u32x4 v = mem[x * 64];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) v[y] &= clean[y];
+                        mem[x * 64] = v;
+                    }
+                }
             }
-        l = l * fade + sum;
+
+            bf16x8 pf[NR][2];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                float top = -__builtin_inff();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fmaxf(s[i][x][0], s[i][x][1]), fmaxf(s[i][x][2], s[i][x][3])));
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                const float now = fmaxf(m[i], top * p.scale_log2);
+                const float ref = now == -__builtin_inff() ? 0.0f : now;   /* no token seen yet */
+                if (__ballot(now != m[i]) != 0) {
+                    const float fade = __builtin_amdgcn_exp2f(m[i] - ref);
+                    l[i] *= fade;
+#pragma unroll
+                    for (int x = 0; x < DT; ++x)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) o[i][x][y] *= fade;
+                    m[i] = now;
+                }
+                float sum = 0.0f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][x][y], p.scale_log2, -ref));
+                        s[i][x][y] = e;
+                        sum += e;
+                    }
+                l[i] += sum;
+                /* weights enter the second product in 16 bits: each is off by up
+                 * to 2^-8 of itself, independently, and the output is rounded as
+                 * far */
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    pf[i][x] = __builtin_bit_cast(bf16x8, u32x4{pack_bf16(s[i][2 * x][0], s[i][2 * x][1]),
+                                                                pack_bf16(s[i][2 * x][2], s[i][2 * x][3]),
+                                                                pack_bf16(s[i][2 * x + 1][0], s[i][2 * x + 1][1]),
+                                                                pack_bf16(s[i][2 * x + 1][2], s[i][2 * x + 1][3])});
+            }
+            wait_vmcnt<KEYS>();
+            const float vs = __builtin_bit_cast(float, *(const uint32_t *)(own + 2 * KB + 768 + 4 * q) << 23);
+            const u32x4 *vals = (const u32x4 *)(own + KB) + lr * 4 + (q ^ (lr >> 2));
+#pragma unroll
+            for (int x = 0; x < DT; ++x) {
+                const u32x4 v = vals[x * 64];
+                const bf16x8 v0 = decode8(v[0], v[1], vs), v1 = decode8(v[2], v[3], vs);
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    o[i][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, pf[i][0], o[i][x], 0, 0, 0);
+                    o[i][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, pf[i][1], o[i][x], 0, 0, 0);
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            copy_values(id1, t1);
+            t0 = t1;
+            kok = kok1;
+            vok = vok1;
+            half ^= 1;
+        }
+        wait_vmcnt<0>();                           /* the copies past the end  */
+    }
+
+    /* join the wavefronts: statistics of all, then sums in halves */
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        l[i] += __shfl_xor(l[i], 16, 64);
+        l[i] += __shfl_xor(l[i], 32, 64);
+        if (q == 0) {
+            st[wave][0][16 * i + lr] = m[i];
+            st[wave][1][16 * i + lr] = l[i];
+        }
+    }
+    __syncthreads();
+    float all[NR], total[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        all[i] = -__builtin_inff();
+        total[i] = 0.0f;
+        for (int w = 0; w < NW; ++w) all[i] = fmaxf(all[i], st[w][0][16 * i + lr]);
+        const float ref = all[i] == -__builtin_inff() ? 0.0f : all[i];
+        for (int w = 0; w < NW; ++w) total[i] += st[w][1][16 * i + lr] * __builtin_amdgcn_exp2f(st[w][0][16 * i + lr] - ref);
+        const float f = __builtin_amdgcn_exp2f(m[i] - ref);
 #pragma unroll
         for (int x = 0; x < DT; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) o[x][y] *= fade;
-        /* weights enter the second product in 16 bits: each is off by up to
-         * 2^-8 of itself, independently, and the output is rounded as far */
-        bf16x8 pf[2];
+            for (int y = 0; y < 4; ++y) o[i][x][y] *= f;
+    }
+    f32x4 *sums = (f32x4 *)store;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-            pf[x] = __builtin_bit_cast(bf16x8, make_uint4(pack_bf16(s[2 * x][0], s[2 * x][1]), pack_bf16(s[2 * x][2], s[2 * x][3]),
-                                                          pack_bf16(s[2 * x + 1][0], s[2 * x + 1][1]),
-                                                          pack_bf16(s[2 * x + 1][2], s[2 * x + 1][3])));
+    for (int half = NW / 2; half >= 1; half /= 2) {
+        if (wave >= half && wave < 2 * half)
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int x = 0; x < DT; ++x) sums[(((wave - half) * NR + i) * DT + x) * 64 + lane] = o[i][x];
+        __syncthreads();
+        if (wave < half)
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int x = 0; x < DT; ++x) o[i][x] += sums[((wave * NR + i) * DT + x) * 64 + lane];
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    const int64_t slot = (((int64_t)blockIdx.z * p.row_tiles + blockIdx.y) * p.splits + blockIdx.x) * NR;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int32_t r = r0 + 16 * i + lr;
+        if (r >= t.rows) continue;
 #pragma unroll
         for (int x = 0; x < DT; ++x) {
-            o[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(vr[x].x, vr[x].y, vs), pf[0], o[x], 0, 0, 0);
-            o[x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(vr[x].z, vr[x].w, vs), pf[1], o[x], 0, 0, 0);
+            if (t.parts > 1)
+                *(f32x4 *)(p.part + ((slot + i) * DT + x) * 256 + lane * 4) = o[i][x];
+            else
+                write_out(p, t, h, r, x, q, o[i][x], all[i], total[i]);
         }
-    }
-
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    /* join the wavefronts */
-    __shared__ float st[kAttnWaves][2][16];
-    __shared__ f32x4 red[kAttnWaves][DT][64];
-    if (q == 0) {
-        st[wave][0][lr] = m;
-        st[wave][1][lr] = l;
-    }
-    __syncthreads();
-    float all = -__builtin_inff();
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) all = fmaxf(all, st[w][0][lr]);
-    const float ref = all == -__builtin_inff() ? 0.0f : all;
-    float total = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) total += st[w][1][lr] * __builtin_amdgcn_exp2f(st[w][0][lr] - ref);
-    const float f = __builtin_amdgcn_exp2f(m - ref);
-#pragma unroll
-    for (int x = 0; x < DT; ++x) {
-        f32x4 v = o[x];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) v[y] *= f;
-        red[wave][x][lane] = v;
-    }
-    __syncthreads();
-    const int64_t slot = ((int64_t)blockIdx.z * p.row_tiles + blockIdx.y) * p.splits + blockIdx.x;
-    for (int32_t x = wave; x < DT; x += kAttnWaves) {
-        f32x4 v = red[0][x][lane];
-#pragma unroll
-        for (int w = 1; w < kAttnWaves; ++w) v += red[w][x][lane];
-        if (t.parts > 1)
-            *(f32x4 *)(p.part + (slot * DT + x) * 256 + lane * 4) = v;
-        else if (r0 + lr < t.rows)
-            write_out<D>(p, t, h, r0 + lr, x, q, v, all, total);
-    }
-    if (t.parts > 1 && threadIdx.x < 16) {
-        p.stat[slot * 32 + lr] = all;
-        p.stat[slot * 32 + 16 + lr] = total;
+        if (t.parts > 1 && q == 0) {
+            p.stat[(slot + i) * 32 + lr] = all[i];
+            p.stat[(slot + i) * 32 + 16 + lr] = total[i];
+        }
     }
 }
 
-/* Parts in ascending order; a wavefront takes 16 channels of the 16 rows. */
-template <int D>
-__global__ __launch_bounds__(D * 4) void attention_combine_kernel(AttnParams p)
+/* Joins the parts of 16 rows and 16 channels: four wavefronts take the parts in
+ * turn, four at a time, and their sums are added in LDS in a fixed order. */
+template <int D, int NR>
+__global__ __launch_bounds__(256) void attention_combine_kernel(AttnParams p)
 {
     constexpr int DT = D / 16;
-    const int32_t lane = threadIdx.x & 63, x = threadIdx.x >> 6, lr = lane & 15, q = lane >> 4;
-    const int32_t b = blockIdx.y / p.c.H, h = blockIdx.y % p.c.H, r0 = blockIdx.x * 16;
-    const Tile t = row_tile(p, b, r0);
-    if (r0 + lr >= t.rows || t.parts == 1) return;
-    const int64_t slot = ((int64_t)blockIdx.y * p.row_tiles + blockIdx.x) * p.splits;
-    float all = -__builtin_inff();
-    for (int32_t i = 0; i < t.parts; ++i) all = fmaxf(all, p.stat[(slot + i) * 32 + lr]);
+    const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, q = lane >> 4;
+    const int32_t x = blockIdx.x % DT, i = blockIdx.x / DT % NR, tile = blockIdx.x / (DT * NR);
+    const int32_t b = blockIdx.y / p.c.H, h = blockIdx.y % p.c.H, r0 = tile * (16 * NR);
+    const Tile t = row_tile(p, b, r0, 16 * NR);
+    if (r0 + 16 * i >= t.rows || t.parts == 1) return;
+    const int32_t r = r0 + 16 * i + lr;
+    const int64_t slot = ((int64_t)blockIdx.y * p.row_tiles + tile) * p.splits;
+    const float *stat = p.stat + (slot * NR + i) * 32 + lr;
+    const float *part = p.part + ((slot * NR + i) * DT + x) * 256 + lane * 4;
+    const bool in = r < t.rows;
+    float m = -__builtin_inff(), l = 0.0f;
+    f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int32_t k = wave; k < t.parts; k += 16) {
+        float pm[4], pl[4];
+        f32x4 v[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            pm[y] = -__builtin_inff();
+            pl[y] = 0.0f;
+            v[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (in && k + 4 * y < t.parts) {
+                pm[y] = stat[(int64_t)(k + 4 * y) * NR * 32];
+                pl[y] = stat[(int64_t)(k + 4 * y) * NR * 32 + 16];
+                v[y] = *(const f32x4 *)(part + (int64_t)(k + 4 * y) * NR * DT * 256);
+            }
+        }
+        const float now = fmaxf(m, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
+        const float ref = now == -__builtin_inff() ? 0.0f : now;
+        const float fade = __builtin_amdgcn_exp2f(m - ref);
+        m = now;
+        l *= fade;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) sum[z] *= fade;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const float f = __builtin_amdgcn_exp2f(pm[y] - ref);
+            l += f * pl[y];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) sum[z] += f * v[y][z];
+        }
+    }
+    __shared__ float st[4][2][64];
+    __shared__ f32x4 sums[4][64];
+    st[wave][0][lane] = m;
+    st[wave][1][lane] = l;
+    sums[wave][lane] = sum;
+    __syncthreads();
+    if (wave != 0 || !in) return;
+    const float all = fmaxf(fmaxf(st[0][0][lane], st[1][0][lane]), fmaxf(st[2][0][lane], st[3][0][lane]));
     const float ref = all == -__builtin_inff() ? 0.0f : all;
     float total = 0.0f;
-    f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int32_t i = 0; i < t.parts; ++i) {
-        const float f = __builtin_amdgcn_exp2f(p.stat[(slot + i) * 32 + lr] - ref);
-        total += f * p.stat[(slot + i) * 32 + 16 + lr];
-        const f32x4 v = *(const f32x4 *)(p.part + ((slot + i) * DT + x) * 256 + lane * 4);
+    f32x4 out = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int y = 0; y < 4; ++y) sum[y] += f * v[y];
+    for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(st[w][0][lane] - ref);
+        const f32x4 v = sums[w][lane];
+        total += f * st[w][1][lane];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) out[z] += f * v[z];
     }
-    write_out<D>(p, t, h, r0 + lr, x, q, sum, all, total);
+    write_out(p, t, h, r, x, q, out, all, total);
 }
 
 namespace {
 
+template <int D, int NR, int NW>
+hipError_t launch_tile(const AttnParams &p, hipStream_t stream)
+{
+    hipLaunchKernelGGL((attention_kernel<D, NR, NW>), dim3((uint32_t)p.splits, (uint32_t)p.row_tiles, (uint32_t)(p.c.B * p.c.H)),
+                       dim3(NW * 64), 0, stream, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    hipLaunchKernelGGL((attention_combine_kernel<D, NR>), dim3((uint32_t)(p.row_tiles * NR * (D / 16)), (uint32_t)(p.c.B * p.c.H)),
+                       dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
 template <int D>
 hipError_t launch_dim(const AttnParams &p, hipStream_t stream)
 {
-    hipLaunchKernelGGL(attention_kernel<D>, dim3((uint32_t)p.splits, (uint32_t)p.row_tiles, (uint32_t)(p.c.B * p.c.H)),
-                       dim3(kAttnWaves * 64), 0, stream, p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL(attention_combine_kernel<D>, dim3((uint32_t)p.row_tiles, (uint32_t)(p.c.B * p.c.H)), dim3(D * 4), 0, stream, p);
-    return hipGetLastError();
+    constexpr int MOST = D == 256 ? 2 : 4;
+    if (p.tile_rows == 16) return launch_tile<D, 1, D == 256 ? 4 : 8>(p, stream);
+    if (p.tile_rows == 32 || MOST == 2) return launch_tile<D, 2, 4>(p, stream);
+    return launch_tile<D, MOST, 4>(p, stream);
 }
 
 } /* namespace */

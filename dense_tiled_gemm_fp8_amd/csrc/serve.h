@@ -38,12 +38,15 @@ struct W4GemmParams {
     int64_t ldx, ldy;             /* elements                                */
     int32_t M;
     int32_t out_bf16;
-    int32_t xvec;                 /* 1: rows of x 16-byte aligned, K % 8 == 0 */
+    int32_t even;                 /* 1: K a multiple of 128, rows of x 16-byte
+                                     aligned, scales and zero points aligned
+                                     and filling whole dwords              */
+    uint32_t spread;              /* set by the launch: 2^32 / workgroups    */
 };
 
 hipError_t launch_w4_quantize(const W4QuantParams &p, hipStream_t stream);
 hipError_t launch_w4_dequantize(const W4QuantParams &p, hipStream_t stream);
-hipError_t launch_w4_gemm(const W4GemmParams &p, int32_t cus, hipStream_t stream);
+hipError_t launch_w4_gemm(const W4GemmParams &p, hipStream_t stream);
 
 /* A paged cache and the step that runs on it (gemm355_kv_cache). */
 struct KvParams {
@@ -75,9 +78,12 @@ struct AttnParams {
     float scale_log2;             /* softmax scale times log2(e)             */
     int32_t Hq, group, D;
     int32_t window, sinks;        /* window 0: none                          */
-    int32_t splits, row_tiles;
-    float *part;                  /* [B H row_tiles][splits][16][D] sums,    */
-    float *stat;                  /* and [..][splits][16][2] maximum and sum */
+    int32_t tile_rows;            /* rows a workgroup: 16, 32 or 64          */
+    int32_t row_tiles;            /* of max_new * group rows                 */
+    int32_t splits;               /* parts of the key axis                   */
+    int32_t part_chunks;          /* least 64-token chunks a part            */
+    float *part;                  /* [B H row_tiles][splits][tile_rows][D]   */
+    float *stat;                  /* sums, and their maxima and totals       */
 };
 
 hipError_t launch_kv_append(const KvAppendParams &p, hipStream_t stream);

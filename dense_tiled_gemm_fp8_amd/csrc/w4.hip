@@ -14,6 +14,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
+#include "dma.h"
 #include "serve.h"
 
 namespace g355 {
@@ -23,6 +26,7 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float bf16_value(uint32_t h) { return __builtin_bit_cast(float, h << 16); }
 
@@ -184,179 +188,82 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(W4QuantParams p)
     }
 }
 
-/*
- * A few rows times a packed matrix.  A workgroup of NW wavefronts owns 16 NT
- * rows of W and 16 MT rows of x; its wavefronts take the 128-wide chunks of K
- * in turn and add up in LDS at the end, so there is one launch and no scratch.
- *
- * v_mfma_f32_16x16x32_bf16 with x as the first operand and the weights as the
- * second: lane l holds column n = l % 16 and 8 consecutive k for the octet
- * q = l / 16, and gets sums of that same column, so a lane needs the scales
- * of one row of W alone.  A lane loads 16 bytes, the 32 codes of octets
- * 4q .. 4q + 3 of its row's chunk.
- *
- * MXFP4: the 32 codes are one block; the conversion to bf16 takes the block's
- * power of two along and stays exact.
- * INT: bf16 holds 16 + u exactly with u in its mantissa (0x4180 | u << 3), so
- * two shifted masks give two weights with no conversion, and
- *   sum_k x (u - z) = sum_k x (16 + u) - (16 + z) sum_k x.
- * The sum of x comes from a product with ones, in the same layout.  16 is the
- * smallest such offset; what the subtraction loses is under two bits of the
- * 32-bit sum.  Scales multiply the group's sum, so weights are never rounded.
- * For groups under 128 a 4 x 4 transpose among the lanes of a row (permlane
- * swaps) first brings octets 4j + q to lane q, so that product j covers the
- * 32 values from 32 j on, and each product lies within one group.
- */
-template <bool MX, int GROUP, int MT, int NT, int NW, bool XVEC>
-__global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
+/* Weights of a dword of codes, in bf16 and in the order that x is put into:
+ * MXFP4 in the codes' order, times the block's power of two; INT 0 2, 4 6,
+ * 1 3, 5 7, as whole numbers.  A byte u = 0 .. 15 read as E4M3 is u * 2^-9
+ * (subnormals and the first binade are one arithmetic sequence), so masked
+ * nibbles convert in pairs: 7 instructions for 8 weights, where shifting each
+ * nibble into a bf16 significand takes 8 and leaves an offset to take off. */
+template <bool MX>
+__device__ __forceinline__ bf16x8 decode_codes(uint32_t w, float s)
 {
-    const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int32_t c = lane & 15, q = lane >> 4;
-    const int32_t n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * MT);
-    const int32_t K = p.w.K, ng = p.w.ng;
-    constexpr bool FLIP = !MX && GROUP < 128;      /* transposed octets        */
-    constexpr int GC = MX ? 1 : 128 / GROUP;       /* groups a chunk           */
-
-    f32x4 acc[NT][MT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const int32_t chunks = (K + 127) >> 7;
-    for (int32_t ch = wave; ch < chunks; ch += NW) {
-        const int32_t kc = ch << 7;
-        uint4 raw[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int32_t n = n0 + 16 * t + c;
-            raw[t] = make_uint4(0, 0, 0, 0);
-            if (n < p.w.N && kc + 32 * q < K)
-                raw[t] = *(const uint4 *)(p.w.codes + (int64_t)n * p.w.ldb + (kc >> 1) + 16 * q);
-        }
-        /* x: row m = lane % 16 of each row tile, 8 values for each of the
-         * chunk's four products */
-        bf16x8 xf[MT][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int32_t m = m0 + 16 * i + c;
-            const uint16_t *row = p.x + (int64_t)m * p.ldx;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int32_t k = kc + (FLIP ? 32 * j + 8 * q : 32 * q + 8 * j);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (XVEC) {
-                    if (m < p.M && k < K) v = *(const uint4 *)(row + k);
-                } else if (m < p.M) {
-                    uint32_t h[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) h[e] = k + e < K ? row[k + e] : 0u;
-                    v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-                }
-                if constexpr (!MX) {
-                    /* the codes' order: value i beside value i + 4 */
-                    v = make_uint4((v.x & 0xFFFFu) | v.z << 16, v.x >> 16 | (v.z & 0xFFFF0000u),
-                                   (v.y & 0xFFFFu) | v.w << 16, v.y >> 16 | (v.w & 0xFFFF0000u));
-                }
-                xf[i][j] = __builtin_bit_cast(bf16x8, v);
-            }
-        }
-        if constexpr (MX) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int32_t n = n0 + 16 * t + c;
-                uint32_t e = 127;
-                if (n < p.w.N && kc + 32 * q < K) e = ((const uint8_t *)p.w.scales)[(int64_t)n * ng + (kc >> 5) + q];
-                const float s = __builtin_bit_cast(float, e << 23);
-                const uint32_t w[4] = {raw[t].x, raw[t].y, raw[t].z, raw[t].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    bf16x2 b[4];
-                    b[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 0);
-                    b[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 1);
-                    b[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 2);
-                    b[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 3);
-                    const bf16x8 wf = __builtin_bit_cast(bf16x8, b);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][j], wf, acc[t][i], 0, 0, 0);
-                }
-            }
-        } else {
-            bf16x8 ones;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ones[e] = (__bf16)1.0f;
-            f32x4 sx[GC][MT];
-#pragma unroll
-            for (int g = 0; g < GC; ++g)
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    sx[g][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int j = 0; j < 4 / GC; ++j)
-                        sx[g][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][g * (4 / GC) + j], ones, sx[g][i], 0, 0, 0);
-                }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int32_t n = n0 + 16 * t + c;
-                uint32_t w[4] = {raw[t].x, raw[t].y, raw[t].z, raw[t].w};
-                if constexpr (FLIP) {
-                    auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                    auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                    auto d = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-                    auto f = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-                    w[0] = d[0];
-                    w[1] = d[1];
-                    w[2] = f[0];
-                    w[3] = f[1];
-                }
-#pragma unroll
-                for (int g = 0; g < GC; ++g) {
-                    float s = 0.0f, off = 24.0f;
-                    if (n < p.w.N && kc + g * GROUP < K) {
-                        const int64_t at = (int64_t)n * ng + kc / GROUP + g;
-                        s = bf16_value(((const uint16_t *)p.w.scales)[at]);
-                        if (p.w.zeros) off = 16.0f + (float)p.w.zeros[at];
-                    }
-                    f32x4 sum[MT];
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int j = g * (4 / GC); j < (g + 1) * (4 / GC); ++j) {
-                        const uint4 b = make_uint4(((w[j] << 3) & 0x00780078u) | 0x41804180u, ((w[j] >> 1) & 0x00780078u) | 0x41804180u,
-                                                   ((w[j] >> 5) & 0x00780078u) | 0x41804180u, ((w[j] >> 9) & 0x00780078u) | 0x41804180u);
-                        const bf16x8 wf = __builtin_bit_cast(bf16x8, b);
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][j], wf, sum[i], 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[t][i][r] += s * __builtin_fmaf(-off, sx[g][i][r], sum[i][r]);
-                }
-            }
-        }
+    bf16x2 b[4];
+    if constexpr (MX) {
+        b[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+        b[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+        b[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+        b[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+    } else {
+        const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+        b[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
+        b[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
+        b[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
+        b[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
     }
+    return __builtin_bit_cast(bf16x8, b);
+}
 
-    /* add the wavefronts' sums; entry (t, i, r, lane) is row 4 (lane / 16) + r,
-     * column lane % 16 of its tile */
-    constexpr int E = NT * MT * 4;
-    __shared__ float red[NW][E][64];
+template <bool MX>
+__device__ __forceinline__ bf16x8 order_x(u32x4 v)
+{
+    if constexpr (!MX)
+        v = u32x4{__builtin_amdgcn_perm(v[1], v[0], 0x05040100u), __builtin_amdgcn_perm(v[3], v[2], 0x05040100u),
+                  __builtin_amdgcn_perm(v[1], v[0], 0x07060302u), __builtin_amdgcn_perm(v[3], v[2], 0x07060302u)};
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+/* 4 x 4 transpose of dwords among the four lanes of a row (lane / 16): lane q
+ * gets dword q of all four. */
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4])
+{
+    auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    auto d = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    auto f = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    w[0] = d[0];
+    w[1] = d[1];
+    w[2] = f[0];
+    w[3] = f[1];
+}
+
+__device__ __forceinline__ bf16x8 ones8()
+{
+    return __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+}
+
+/* The wavefronts' sums, added in order and stored: entry (t, i, r, lane) is
+ * row m0 + 16 i + 4 (lane / 16) + r (R = 1: m0 + lane / 16), column
+ * n0 + 16 t + lane % 16. */
+template <int NT, int RT, int R, int NW>
+__device__ __forceinline__ void store_sums(const W4GemmParams &p, float *store, int32_t wave, int32_t lane, int32_t m0, int32_t n0,
+                                           const f32x4 (&acc)[NT][RT])
+{
+    constexpr int E = NT * RT * R;
+    float(*red)[E][64] = (float(*)[E][64])store;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) red[wave][(t * MT + i) * 4 + r][lane] = acc[t][i][r];
+            for (int r = 0; r < R; ++r) red[wave][(t * RT + i) * R + r][lane] = acc[t][i][r];
     __syncthreads();
     for (int32_t e = threadIdx.x; e < E * 64; e += NW * 64) {
         const int32_t el = e >> 6, ln = e & 63;
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) sum += red[w][el][ln];
-        const int32_t t = el / (MT * 4), i = el / 4 % MT, r = el & 3;
-        const int32_t m = m0 + 16 * i + 4 * (ln >> 4) + r, n = n0 + 16 * t + (ln & 15);
+        const int32_t t = el / (RT * R), i = el / R % RT, r = el % R;
+        const int32_t m = m0 + 16 * i + (R == 4 ? 4 * (ln >> 4) + r : ln >> 4), n = n0 + 16 * t + (ln & 15);
         if (m < p.M && n < p.w.N) {
             if (p.out_bf16)
                 ((__bf16 *)p.y)[(int64_t)m * p.ldy + n] = (__bf16)sum;
@@ -364,6 +271,286 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
                 ((float *)p.y)[(int64_t)m * p.ldy + n] = sum;
         }
     }
+}
+
+/*
+ * A few rows times a packed matrix.  A workgroup of NW wavefronts owns 16 NT
+ * rows of W and up to 16 MT rows of x; its wavefronts take a run of the
+ * 128-wide chunks of K each and add up in LDS at the end, so there is one
+ * launch, no scratch, and each code is read once for 16 MT rows.
+ *
+ * v_mfma_f32_16x16x32_bf16 with x as the first operand and the weights as the
+ * second: lane l holds column n = l % 16 and 8 consecutive k for the octet
+ * q = l / 16, and gets sums of that same column, so a lane needs the scales
+ * of one row of W alone.  A lane takes 16 bytes, the 32 codes of octets
+ * 4q .. 4q + 3 of its row's chunk.
+ *
+ * MXFP4: the 32 codes are one block; the conversion to bf16 takes the block's
+ * power of two along and stays exact.
+ * INT: sum_k x (u - z) = sum_k x u - z sum_k x; the sum of x comes from a
+ * product with ones, in the same layout.  Scales multiply the group's sum, so
+ * weights are never rounded.  For groups under 128 a transpose among the lanes
+ * of a row first brings octets 4j + q to lane q, so that product j covers the
+ * 32 values from 32 j on, and each product lies within one group.
+ *
+ * The vector memory unit takes four lanes at a time and wants their 64 bytes
+ * contiguous; the matrix instruction wants consecutive lanes in different
+ * rows.  So copies go straight to LDS with lanes along rows (four lanes a row
+ * of a chunk's codes, 16 a row of x) and each wavefront reads its own copies
+ * back in the matrix order.  The 16-byte units of a row are exchanged by row
+ * number, which leaves the reads free of bank conflicts.  Loads in the matrix
+ * order took 64 cycles each instead of 16.
+ *
+ * A wavefront has up to four chunks in LDS, one read while the others arrive; it
+ * waits for its own copies alone, so there is no barrier in the loop.
+ *
+ * Rows of x past M and of W past N are read as the last ones (their sums are
+ * not stored), which leaves the loop without masks.  MT = 0 is for M <= 4: row
+ * m sits in row 4m of the instruction's 16, so a lane scales one sum, not four.
+ * K is a multiple of 128, rows are 16-byte aligned, scales and zero points
+ * fill whole dwords.
+ */
+template <bool MX, int GROUP, bool ZEROS, int MT, int NT, int NW>
+__global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
+{
+    constexpr int RT = MT ? MT : 1;                /* row tiles                */
+    constexpr int R = MT ? 4 : 1;                  /* sums of a tile in a lane */
+    constexpr bool FLIP = !MX && GROUP < 128;      /* transposed octets        */
+    constexpr int GC = MX ? 1 : 128 / GROUP;       /* groups a chunk           */
+    constexpr int XL = MT ? 4 * MT : 1;            /* copies of x a chunk      */
+    constexpr int SD = GC == 4 ? 2 : 1;            /* dwords of scales a row   */
+    constexpr int COPIES = NT + XL;                /* of a chunk               */
+    constexpr int SLOT = COPIES * 1024;
+    constexpr int QUAD = NT * (SD + ZEROS) * 256;  /* scales of four chunks    */
+    constexpr int FIT = ((MT ? 163840 : 81920) / NW - 2 * QUAD) / SLOT, DEPTH = FIT < 4 ? FIT : 4;
+    constexpr int OWN = DEPTH * SLOT + 2 * QUAD;
+    static_assert(NT * RT * R * 256 <= OWN && DEPTH >= 2 && COPIES * (DEPTH - 1) < 64, "LDS and waits");
+    const int32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t c = lane & 15, q = lane >> 4;
+    const int32_t n0 = blockIdx.x * (16 * NT), m0 = blockIdx.y * (16 * RT);
+    const int32_t K = p.w.K, ng = p.w.ng;
+
+    /* per-lane offsets from the workgroup's first rows (64 rows stay under
+     * 2^31 bytes: K is at most 2^24) */
+    const int32_t lrow = lane >> 2, lpiece = (lane & 3) ^ (lrow >> 2);
+    uint32_t code_at[NT], x_at[XL];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        code_at[t] = (uint32_t)((min(n0 + 16 * t + lrow, p.w.N - 1) - n0) * (int32_t)p.w.ldb + 16 * lpiece);
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+        const int32_t row = 4 * i + (lane >> 4);
+        x_at[i] = (uint32_t)((min(m0 + row, p.M - 1) - m0) * (int32_t)p.ldx + 8 * ((lane & 15) ^ (row & 15))) * 2;
+    }
+    const i32x4 rc = rsrc_words(p.w.codes + (int64_t)n0 * p.w.ldb);
+    const i32x4 rs = rsrc_words((const uint8_t *)p.w.scales + (int64_t)n0 * ng * (MX ? 1 : 2));
+    const i32x4 rz = rsrc_words(ZEROS ? p.w.zeros + (int64_t)n0 * ng : p.w.codes);
+    const i32x4 rx = rsrc_words(p.x + (int64_t)m0 * p.ldx);
+
+    __shared__ __align__(16) uint8_t store[NW * OWN];
+    const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(store) + wave * OWN);
+    const uint8_t *own = store + wave * OWN;
+
+    /* A wavefront takes a run of chunks, so that its copies in flight are
+     * neighbours in memory, and begins it at a place of the workgroup's own, so
+     * that workgroups spread over the memory channels: rows are often a power
+     * of two apart. */
+    const int32_t chunks = K >> 7;
+    const int32_t first = chunks * wave / NW;
+    const int32_t count = chunks * (wave + 1) / NW - first;
+    const int32_t start = (int32_t)__umulhi(blockIdx.x * p.spread, (uint32_t)count);
+    auto chunk = [&](int32_t i) __attribute__((always_inline)) {
+        const int32_t ch = i + start;
+        return first + (ch >= count ? ch - count : ch);
+    };
+
+    /* A chunk's copies into a slot; past the last chunk they read nothing. */
+    auto copy = [&](int32_t slot, int32_t i) __attribute__((always_inline)) {
+        const uint32_t at = base + (uint32_t)slot * SLOT;
+        const uint32_t ch = (uint32_t)chunk(i), kb = i < count ? ch << 6 : kOOB, kx = i < count ? ch << 8 : kOOB;
+        unroll<NT>([&](auto t) { dma16<t * 1024>(rc, at, code_at[t] + kb); });
+        unroll<XL>([&](auto i) { dma16<(NT + i) * 1024>(rx, at, x_at[i] + kx); });
+    };
+    /* Scales of the run's chunks i .. i + 3 (the last again past its end): lane
+     * 4r + d copies row r's of chunk i + d.  Rows are far apart, so each of
+     * these copies touches 16 lines for a few bytes of each; by fours they
+     * touch a quarter as many. */
+    auto copy_scales = [&](int32_t half, int32_t i) __attribute__((always_inline)) {
+        const uint32_t at = base + DEPTH * SLOT + (uint32_t)half * QUAD;
+        const int32_t ch = chunk(min(i + (lane & 3), count - 1));
+        unroll<NT>([&](auto t) {
+            const uint32_t si = (uint32_t)((min(n0 + 16 * t + lrow, p.w.N - 1) - n0) * ng + ch * (MX ? 4 : GC));
+            const uint32_t ks = MX ? si : 2 * si & ~3u;
+            constexpr int PER = (SD + ZEROS) * 256;
+            dma4(rs, at + t * PER, ks);
+            if constexpr (SD == 2) dma4(rs, at + t * PER + 256, ks + 4);
+            if constexpr (ZEROS) dma4(rz, at + t * PER + SD * 256, si & ~3u);
+        });
+    };
+
+    f32x4 acc[NT][RT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int32_t code_get = c * 64 + ((q ^ (c >> 2)) << 4);
+    const int32_t xrow = MT ? c : c >> 2;
+    if (count > 0) {
+        copy_scales(0, 0);
+#pragma unroll
+        for (int d = 0; d < DEPTH - 1; ++d) copy(d, d);
+    }
+    int32_t slot = 0, free_slot = DEPTH - 1;
+#pragma unroll 1
+    for (int32_t i = 0; i < count; ++i) {
+        /* the slot to fill is the one read in the step before: those reads
+         * have returned */
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if ((i & 3) == 0 && i + 4 < count) copy_scales((i >> 2 & 1) ^ 1, i + 4);
+        copy(free_slot, i + DEPTH - 1);
+        /* all but the copies of the next DEPTH - 1 chunks: this chunk's, and
+         * scales sent off four steps ago */
+        wait_vmcnt<(DEPTH - 1) * COPIES>();
+        const uint8_t *in = own + slot * SLOT, *xin = in + NT * 1024;
+        const uint8_t *sin = own + DEPTH * SLOT + (i >> 2 & 1) * QUAD + 4 * (4 * c + (i & 3));
+        const int32_t ch = chunk(i);
+        uint32_t w[NT][4], sc[NT][SD], zp[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const u32x4 v = *(const u32x4 *)(in + t * 1024 + code_get);
+            w[t][0] = v[0];
+            w[t][1] = v[1];
+            w[t][2] = v[2];
+            w[t][3] = v[3];
+            if constexpr (FLIP) transpose4(w[t]);
+            const int32_t row = 16 * t + c;
+            zp[t] = 0x08080808u;
+            const uint8_t *st = sin + t * ((SD + ZEROS) * 256);
+            sc[t][0] = *(const uint32_t *)st;
+            if constexpr (SD == 2) sc[t][1] = *(const uint32_t *)(st + 256);
+            if constexpr (ZEROS) zp[t] = *(const uint32_t *)(st + SD * 256);
+            if constexpr (MX) {
+                sc[t][0] = sc[t][0] >> (8 * q) & 0xFFu;
+            } else if constexpr (GC < 4) {
+                /* the dword may begin before this chunk's part of it */
+                const uint32_t at = (uint32_t)((min(n0 + row, p.w.N - 1) - n0) * ng + ch * GC);
+                if constexpr (GC == 1) sc[t][0] >>= 16 * (at & 1);
+                if constexpr (ZEROS) zp[t] >>= 8 * (at & 3);
+            }
+        }
+        f32x4 sum[NT][RT], sx[RT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!MX && j % (4 / GC) == 0) {
+#pragma unroll
+                for (int i2 = 0; i2 < RT; ++i2) {
+                    sx[i2] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) sum[t][i2] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+            }
+            bf16x8 xf[RT];
+#pragma unroll
+            for (int i2 = 0; i2 < RT; ++i2) {
+                xf[i2] = order_x<MX>(*(const u32x4 *)(xin + (16 * i2 + xrow) * 256 + (((FLIP ? 4 * j + q : 4 * q + j) ^ xrow) << 4)));
+                if constexpr (!MX) sx[i2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i2], ones8(), sx[i2], 0, 0, 0);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const bf16x8 wf = decode_codes<MX>(w[t][j], __builtin_bit_cast(float, sc[t][0] << 23));
+#pragma unroll
+                for (int i2 = 0; i2 < RT; ++i2) {
+                    if constexpr (MX)
+                        acc[t][i2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i2], wf, acc[t][i2], 0, 0, 0);
+                    else
+                        sum[t][i2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i2], wf, sum[t][i2], 0, 0, 0);
+                }
+            }
+            if (!MX && j % (4 / GC) == 4 / GC - 1) {
+                const int g = j / (4 / GC);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t two = sc[t][g >> 1];
+                    const float s = __builtin_bit_cast(float, g & 1 ? two & 0xFFFF0000u : two << 16);
+                    const float z = (float)((zp[t] >> (8 * g)) & 0xFFu);
+#pragma unroll
+                    for (int i2 = 0; i2 < RT; ++i2)
+#pragma unroll
+                        for (int r = 0; r < R; ++r) acc[t][i2][r] += s * __builtin_fmaf(-z, sx[i2][r], sum[t][i2][r]);
+                }
+            }
+        }
+        free_slot = slot;
+        slot = slot + 1 == DEPTH ? 0 : slot + 1;
+    }
+    wait_vmcnt<0>();                               /* copies that read nothing */
+    __syncthreads();
+    store_sums<NT, RT, R, NW>(p, (float *)store, wave, lane, m0, n0, acc);
+}
+
+/* The same product for what the kernel above does not take (K not a multiple of
+ * 128, unaligned rows): 16 rows of W and of x a workgroup, operands loaded in
+ * the matrix order, elements past K read as zero. */
+constexpr int kW4AnyWaves = 8;
+
+template <bool MX, int GROUP>
+__global__ __launch_bounds__(kW4AnyWaves * 64) void w4_gemm_any_kernel(W4GemmParams p)
+{
+    constexpr bool FLIP = !MX && GROUP < 128;
+    constexpr int GC = MX ? 1 : 128 / GROUP;
+    const int32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t c = lane & 15, q = lane >> 4;
+    const int32_t n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
+    const int32_t K = p.w.K, n = min(n0 + c, p.w.N - 1), m = min(m0 + c, p.M - 1);
+    const uint8_t *row = p.w.codes + (int64_t)n * p.w.ldb;
+    const uint16_t *x = p.x + (int64_t)m * p.ldx;
+    const int64_t g0 = (int64_t)n * p.w.ng;
+    __shared__ float store[kW4AnyWaves * 4 * 64];
+
+    f32x4 acc[1][1];
+    acc[0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int32_t kc = wave << 7; kc < K; kc += kW4AnyWaves << 7) {
+        u32x4 raw = {0, 0, 0, 0};
+        if (kc + 32 * q < K) raw = *(const u32x4 *)(row + (kc >> 1) + 16 * q);
+        uint32_t w[4] = {raw[0], raw[1], raw[2], raw[3]};
+        if constexpr (FLIP) transpose4(w);
+        bf16x8 xf[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int32_t k = kc + (FLIP ? 32 * j + 8 * q : 32 * q + 8 * j);
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = k + e < K ? x[k + e] : 0u;
+            xf[j] = order_x<MX>(u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16});
+        }
+        if constexpr (MX) {
+            const uint32_t e = kc + 32 * q < K ? ((const uint8_t *)p.w.scales)[g0 + (kc >> 5) + q] : 127u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[0][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j], decode_codes<MX>(w[j], __builtin_bit_cast(float, e << 23)),
+                                                                    acc[0][0], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int g = 0; g < GC; ++g) {
+                float s = 0.0f, z = 8.0f;
+                if (kc + g * GROUP < K) {
+                    const int64_t at = g0 + kc / GROUP + g;
+                    s = bf16_value(((const uint16_t *)p.w.scales)[at]);
+                    if (p.w.zeros) z = (float)p.w.zeros[at];
+                }
+                f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f}, sx = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = g * (4 / GC); j < (g + 1) * (4 / GC); ++j) {
+                    sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j], ones8(), sx, 0, 0, 0);
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j], decode_codes<MX>(w[j], 0.0f), sum, 0, 0, 0);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[0][0][r] += s * __builtin_fmaf(-z, sx[r], sum[r]);
+            }
+        }
+    }
+    store_sums<1, 1, 4, kW4AnyWaves>(p, store, wave, lane, m0, n0, acc);
 }
 
 hipError_t launch_w4_quantize(const W4QuantParams &p, hipStream_t stream)
@@ -382,40 +569,58 @@ hipError_t launch_w4_dequantize(const W4QuantParams &p, hipStream_t stream)
 
 namespace {
 
-template <bool MX, int GROUP, int MT, int NT, int NW>
+template <bool MX, int GROUP, bool ZEROS, int MT, int NT, int NW>
 void launch_one(const W4GemmParams &p, hipStream_t stream)
 {
-    const dim3 grid((uint32_t)((p.w.N + 16 * NT - 1) / (16 * NT)), (uint32_t)((p.M + 16 * MT - 1) / (16 * MT)));
-    if (p.xvec)
-        hipLaunchKernelGGL((w4_gemm_kernel<MX, GROUP, MT, NT, NW, true>), grid, dim3(NW * 64), 0, stream, p);
-    else
-        hipLaunchKernelGGL((w4_gemm_kernel<MX, GROUP, MT, NT, NW, false>), grid, dim3(NW * 64), 0, stream, p);
+    const int32_t rows = MT ? 16 * MT : 16;
+    const dim3 grid((uint32_t)((p.w.N + 16 * NT - 1) / (16 * NT)), (uint32_t)((p.M + rows - 1) / rows));
+    W4GemmParams q = p;
+    q.spread = (uint32_t)(0xFFFFFFFFu / grid.x);
+    hipLaunchKernelGGL((w4_gemm_kernel<MX, GROUP, ZEROS, MT, NT, NW>), grid, dim3(NW * 64), 0, stream, q);
 }
 
-template <bool MX, int GROUP>
-void launch_rows(const W4GemmParams &p, int32_t cus, hipStream_t stream)
+template <bool MX, int GROUP, bool ZEROS>
+void launch_rows(const W4GemmParams &p, hipStream_t stream)
 {
-    (void)cus;
-    if (p.M <= 16)
-        launch_one<MX, GROUP, 1, 1, 8>(p, stream);
-    else if (p.M <= 32)
-        launch_one<MX, GROUP, 2, 2, 8>(p, stream);
-    else
-        launch_one<MX, GROUP, 4, 2, 4>(p, stream);
+    if (!p.even) {
+        const dim3 grid((uint32_t)((p.w.N + 15) / 16), (uint32_t)((p.M + 15) / 16));
+        hipLaunchKernelGGL((w4_gemm_any_kernel<MX, GROUP>), grid, dim3(kW4AnyWaves * 64), 0, stream, p);
+    } else if (p.M <= 4) {
+        if (p.w.N >= 8192)
+            launch_one<MX, GROUP, ZEROS, 0, 2, 8>(p, stream);
+        else
+            launch_one<MX, GROUP, ZEROS, 0, 1, 8>(p, stream);
+    } else if (p.M <= 16) {
+        if (p.w.N >= 16384)
+            launch_one<MX, GROUP, ZEROS, 1, 4, 4>(p, stream);
+        else if (p.w.N >= 8192)
+            launch_one<MX, GROUP, ZEROS, 1, 2, 8>(p, stream);
+        else
+            launch_one<MX, GROUP, ZEROS, 1, 1, 8>(p, stream);
+    } else if (p.M <= 32) {
+        if (p.w.N >= 16384)
+            launch_one<MX, GROUP, ZEROS, 2, 4, 4>(p, stream);
+        else if (p.w.N >= 8192)
+            launch_one<MX, GROUP, ZEROS, 2, 2, 4>(p, stream);
+        else
+            launch_one<MX, GROUP, ZEROS, 2, 1, 4>(p, stream);
+    } else {
+        launch_one<MX, GROUP, ZEROS, 4, 2, 4>(p, stream);
+    }
 }
 
 } /* namespace */
 
-hipError_t launch_w4_gemm(const W4GemmParams &p, int32_t cus, hipStream_t stream)
+hipError_t launch_w4_gemm(const W4GemmParams &p, hipStream_t stream)
 {
     if (p.w.mx)
-        launch_rows<true, 32>(p, cus, stream);
+        launch_rows<true, 32, false>(p, stream);
     else if (p.w.group == 32)
-        launch_rows<false, 32>(p, cus, stream);
+        p.w.zeros ? launch_rows<false, 32, true>(p, stream) : launch_rows<false, 32, false>(p, stream);
     else if (p.w.group == 64)
-        launch_rows<false, 64>(p, cus, stream);
+        p.w.zeros ? launch_rows<false, 64, true>(p, stream) : launch_rows<false, 64, false>(p, stream);
     else
-        launch_rows<false, 128>(p, cus, stream);
+        p.w.zeros ? launch_rows<false, 128, true>(p, stream) : launch_rows<false, 128, false>(p, stream);
     return hipGetLastError();
 }
 

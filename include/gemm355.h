@@ -588,8 +588,8 @@ GEMM355_API gemm355_status gemm355_w4_dequantize(const gemm355_w4_matrix *q, voi
  * same bits from the same arguments every time.  M or N = 0: nothing is done;
  * K = 0: y = 0.
  * Errors: EINVAL (sizes, leading dimensions, enums, null pointers, y
- * overlapping an input), EALIGN, EUNSUPPORTED (N or K above 2^30, M above
- * 2^19), EHIP.
+ * overlapping an input), EALIGN, EUNSUPPORTED (N above 2^30, M above 2^19, ldx
+ * or ldw above 2^24), EHIP.
  */
 GEMM355_API gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx,
                                const gemm355_w4_matrix *w, void *y, int64_t ldy,

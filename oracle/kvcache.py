@@ -116,24 +116,25 @@ def attention(step: Step, k: np.ndarray, v: np.ndarray, ks: np.ndarray, vs: np.n
     lse = np.full((rows, Hq), np.nan)
     S = np.full((rows, Hq), np.nan)
     for b in range(step.batch):
+        ids = [step.page_id(b, t) for t in range(step.len[b])]
+        held = np.array([t for t, a in enumerate(ids) if a is not None], dtype=np.int64)
+        pg, sl = np.array([ids[t] for t in held], dtype=np.int64), held % step.page
+        kk = decode(k[pg, :, sl]) * np.ldexp(1.0, ks[pg].astype(int) - 127)[..., None]       # tokens, H, D
+        vv = decode(v[pg, :, :, sl]) * np.ldexp(1.0, vs[pg].astype(int) - 127)[..., None]
         for i in range(step.new[b]):
             p, r = step.len[b] - step.new[b] + i, step.row[b] + i
-            seen = [t for t in range(max(p + 1, 0)) if window == 0 or t > p - window or t < sinks]
-            at = [(step.page_id(b, t), t % step.page) for t in seen]
-            at = [(a, t) for a, t in at if a is not None]
+            seen = (held <= p) & ((held > p - window) | (held < sinks) if window else True)
             for j in range(Hq):
                 h = j // (Hq // H)
-                if not at:
+                if not seen.any():
                     o[r, j], W[r, j], lse[r, j], S[r, j] = 0.0, 0.0, -np.inf, 0.0
                     continue
-                pg, sl = np.array([a for a, _ in at]), np.array([t for _, t in at])
-                kk = decode(k[pg, h, sl]) * np.ldexp(1.0, ks[pg, h].astype(int) - 127)[:, None]
-                vv = decode(v[pg, h, :, sl]) * np.ldexp(1.0, vs[pg, h].astype(int) - 127)[:, None]
-                x = scale * (kk @ q[r, j])
+                keys, vals = kk[seen, h], vv[seen, h]
+                x = scale * (keys @ q[r, j])
                 m = x.max()
                 w = np.exp(x - m)
-                o[r, j] = w @ vv / w.sum()
-                W[r, j] = w @ np.abs(vv) / w.sum()
+                o[r, j] = w @ vals / w.sum()
+                W[r, j] = w @ np.abs(vals) / w.sum()
                 lse[r, j] = m + np.log(w.sum())
-                S[r, j] = float(np.max(scale * (np.abs(kk) @ np.abs(q[r, j]))))
+                S[r, j] = float(np.max(scale * (np.abs(keys) @ np.abs(q[r, j]))))
     return o, lse, W, S

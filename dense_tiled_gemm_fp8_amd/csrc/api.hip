@@ -551,7 +551,7 @@ gemm355_status check_kv(const gemm355_kv_cache &c, KvParams &k)
     if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256) return GEMM355_EUNSUPPORTED;
     if (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128) return GEMM355_EUNSUPPORTED;
     if (c.pages > 0x7FFFFFFF || c.tokens > kMaxDim || c.max_new > kMaxDim || c.max_len > kMaxDim || c.table_ld > kMaxDim ||
-        c.batch > 65535 || c.batch * c.heads > 65535)
+        c.batch > 65528 || c.batch * c.heads > 65528)
         return GEMM355_EUNSUPPORTED;
     const int64_t ld = c.table_ld ? c.table_ld : (c.max_len + c.page - 1) / c.page;
     if (c.max_len > ld * c.page) return GEMM355_EINVAL;
@@ -650,6 +650,7 @@ gemm355_status append_setup(const gemm355_kv_append_args *a, KvAppendParams &p)
     p.D = c.head_dim;
     p.rot = a->rot_dim;
     p.interleaved = a->interleaved ? 1 : 0;
+    p.whole = a->rot_dim % 16 == 0 && aligned(a->cos, 16) && aligned(a->sin, 16) ? 1 : 0;
     return GEMM355_OK;
 }
 
@@ -680,13 +681,13 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     p.window = a->window >= c.max_len ? 0 : (int32_t)a->window;
     p.sinks = (int32_t)std::min<int64_t>(a->sinks, c.max_len);
     const int64_t rows = (int64_t)p.c.max_new * p.group;
-    p.tile_rows = rows <= 16 ? 16 : rows <= 32 || p.D == 256 ? 32 : 64;
+    p.tile_rows = rows <= 16 ? 16 : 32;
     if (rows > (int64_t)16 * 65535) return GEMM355_EUNSUPPORTED;
     p.row_tiles = (int32_t)((rows + p.tile_rows - 1) / p.tile_rows);
     const int64_t tiles = std::max<int64_t>(1, c.batch * c.heads * p.row_tiles);
     int64_t seen = c.max_len;
     if (p.window) seen = std::min(seen, (int64_t)p.window + p.c.max_new + p.sinks + 128);
-    p.part_chunks = a->splits ? 4 : 24;
+    p.part_chunks = a->splits ? 4 : 16;
     const int64_t most = std::max<int64_t>(1, (seen + 64 * p.part_chunks - 1) / (64 * p.part_chunks));
     const int32_t cus = [] {
         int n = 0;
@@ -696,7 +697,9 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
         }
         return device_cus();
     }();
-    const int64_t want = a->splits ? a->splits : (2 * (int64_t)cus + tiles - 1) / tiles;
+    /* workgroups that fill the device once: their LDS leaves room for one a
+     * compute unit, two where heads are small */
+    const int64_t want = a->splits ? a->splits : ((p.D == 64 ? 2 : 1) * (int64_t)cus + tiles - 1) / tiles;
     p.splits = (int32_t)std::min(want, most);
     const int64_t slots = tiles * p.splits;
     bytes = p.splits > 1 ? (size_t)slots * (size_t)p.tile_rows * (size_t)(p.D + 2) * sizeof(float) : 0;

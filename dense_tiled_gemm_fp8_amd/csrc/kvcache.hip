@@ -19,6 +19,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "dma.h"
 #include "serve.h"
 
@@ -69,47 +71,67 @@ __device__ __forceinline__ Seq sequence(const KvParams &c, int32_t b)
 
 /* ---------------------------------------------------------------- append */
 
+__device__ __forceinline__ void unpack8(u32x4 a, float (&v)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t w = a[j];
+        v[2 * j] = __builtin_bit_cast(float, w << 16);
+        v[2 * j + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
+    }
+}
+
+/* a c - b s or, for the second of a pair, a c + b s.  The products of a 16-bit
+ * and a 32-bit value are exact in 64 bits, so each result is rounded to 32
+ * bits once. */
+__device__ __forceinline__ float turned(float a, float b, float c, float s, bool second)
+{
+    const double bs = (double)b * (double)s;
+    return (float)((double)a * (double)c + (second ? bs : -bs));
+}
+
 /* 8 values of channels d0 .. d0 + 7 of one token's head at x, rotated for
- * position pos: pairs (a, b) become (a cos - b sin, b cos + a sin).  The
- * products of a 16-bit and a 32-bit value are exact in 64 bits, so each
- * result is rounded to 32 bits once. */
+ * position pos: pairs (a, b) become (a cos - b sin, b cos + a sin). */
 __device__ __forceinline__ void rotate8(const KvAppendParams &p, const uint16_t *x, int32_t d0, int32_t pos, float (&v)[8])
 {
     const int32_t half = p.rot >> 1;
     const float *cs = p.cos + (int64_t)pos * half, *sn = p.sin + (int64_t)pos * half;
+    unpack8(*(const u32x4 *)(x + d0), v);
+    if (p.whole) {
+        /* 16 channels' pairs or none in each 8: everything by vectors */
+        if (d0 >= p.rot) return;
+        if (p.interleaved) {
+            const f32x4 c = *(const f32x4 *)(cs + d0 / 2), s = *(const f32x4 *)(sn + d0 / 2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = v[2 * j], b = v[2 * j + 1], cj = c[j], sj = s[j];
+                v[2 * j] = turned(a, b, cj, sj, false);
+                v[2 * j + 1] = turned(b, a, cj, sj, true);
+            }
+        } else {
+            const bool second = d0 >= half;
+            const int32_t i = second ? d0 - half : d0;
+            float w[8];
+            unpack8(*(const u32x4 *)(x + (second ? i : d0 + half)), w);
+            const f32x4 c0 = *(const f32x4 *)(cs + i), c1 = *(const f32x4 *)(cs + i + 4);
+            const f32x4 s0 = *(const f32x4 *)(sn + i), s1 = *(const f32x4 *)(sn + i + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float ca = c0[j], cb = c1[j], sa = s0[j], sb = s1[j];
+                v[j] = turned(v[j], w[j], ca, sa, second);
+                v[j + 4] = turned(v[j + 4], w[j + 4], cb, sb, second);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int32_t d = d0 + j;
-        const double a = bf16_value(x[d]);
-        if (d >= p.rot) {
-            v[j] = (float)a;
-        } else {
-            int32_t other, i;
-            bool second;
-            if (p.interleaved) {
-                second = d & 1;
-                other = d ^ 1;
-                i = d >> 1;
-            } else {
-                second = d >= half;
-                other = second ? d - half : d + half;
-                i = second ? d - half : d;
-            }
-            const double b = bf16_value(x[other]);
-            const double c = cs[i], s = sn[i];
-            v[j] = (float)(second ? a * c + b * s : a * c - b * s);
-        }
-    }
-}
-
-__device__ __forceinline__ void plain8(const uint16_t *x, int32_t d0, float (&v)[8])
-{
-    const uint4 a = *(const uint4 *)(x + d0);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __builtin_bit_cast(float, w[j] << 16);
-        v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+        if (d >= p.rot) continue;
+        const bool second = p.interleaved ? d & 1 : d >= half;
+        const int32_t other = p.interleaved ? d ^ 1 : second ? d - half : d + half;
+        const int32_t i = p.interleaved ? d >> 1 : second ? d - half : d;
+        v[j] = turned(v[j], bf16_value(x[other]), cs[i], sn[i], second);
     }
 }
 
@@ -143,9 +165,16 @@ __device__ __forceinline__ int32_t block_exponent(float a)
 
 } /* namespace */
 
-/* One workgroup for the new tokens of one page, head and of keys or values
- * (reads them twice: for their largest magnitude, then to write codes); the
- * workgroups behind those rotate q. */
+/* Work of the append: workgroups 0 .. kv_units - 1 each write the new tokens of
+ * one page, head and of keys or values; those behind rotate q, 256 octets of
+ * channels each.
+ *
+ * A page's new tokens stay in registers (ITEMS octets a thread) between finding
+ * their largest magnitude and encoding them, so they are read once; values go
+ * through LDS as codes to lie along tokens.  What takes the time of a step of
+ * single tokens is the chain lengths -> page id -> scale, each a load that
+ * waits for the one before: tokens and tables are loaded beside it. */
+template <int ITEMS>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_t pages_each, int32_t kv_units, int32_t q_blocks)
 {
     const KvParams &c = p.c;
@@ -163,12 +192,16 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
         if (p.rot)
             rotate8(p, x, d0, s.pos + i, v);
         else
-            plain8(x, d0, v);
-        *(uint4 *)(p.q_out + (s.row + i) * p.ldqo + head * D + d0) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+            unpack8(*(const u32x4 *)(x + d0), v);
+        *(u32x4 *)(p.q_out + (s.row + i) * p.ldqo + head * D + d0) =
+            u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
         return;
     }
     __shared__ float red[4];
+    /* codes of values, by channel: the new tokens' slots from a multiple of 16
+     * to one (at most 30 more than there are tokens, of which D times as many as
+     * 2048 ITEMS at most), and four bytes that spread channels over the banks */
+    __shared__ __align__(16) uint8_t codes[ITEMS * 2048 + 34 * 256];
     int32_t u = blockIdx.x;
     const bool keys = (u & 1) == 0;
     u >>= 1;
@@ -181,27 +214,33 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
     const int32_t lo = max(first, base), hi = min(s.len, base + c.page);
     if (s.n == 0 || lo >= hi) return;
     const int32_t id = c.table[(int64_t)b * c.table_ld + pg];
+    const uint16_t *x = keys ? p.xk + h * D : p.xv + h * D;
+    const int64_t ld = keys ? p.ldk : p.ldv;
+    const bool turn = keys && p.rot != 0;
+
+    float v[ITEMS][8];
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int32_t w = k * 256 + (int32_t)threadIdx.x, t = lo + w / oct, d0 = w % oct * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
+        if (t < hi) {
+            const uint16_t *row = x + (s.row + t - s.pos) * ld;
+            if (turn)
+                rotate8(p, row, d0, t, v[k]);
+            else
+                unpack8(*(const u32x4 *)(row + d0), v[k]);
+        }
+    }
     if (id < 0 || id >= c.pages) return;
     const int64_t block = (int64_t)id * c.H + h;
     uint8_t *scale = (keys ? c.k_scale : c.v_scale) + block;
     const int32_t e_old = (int32_t)*scale - 127;
-    const uint16_t *x = keys ? p.xk + h * D : p.xv + h * D;
-    const int64_t ld = keys ? p.ldk : p.ldv;
-    const bool turn = keys && p.rot != 0;
-    const int32_t count = hi - lo;
-
-    float m = 0.0f;
-    for (int32_t w = threadIdx.x; w < count * oct; w += 256) {
-        const int32_t t = lo + w / oct, d0 = w % oct * 8;
-        const uint16_t *row = x + (s.row + t - s.pos) * ld;
-        float v[8];
-        if (turn)
-            rotate8(p, row, d0, t, v);
-        else
-            plain8(row, d0, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-    }
+    for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[k][i]));
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
@@ -210,62 +249,76 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
     int32_t e = block_exponent(m);
     const bool begins = lo == base;
     if (!begins) e = max(e, e_old);
-    /* the block's older tokens, where its scale grew */
-    const int32_t from = !begins && e > e_old ? 0 : lo - base;
+    const bool grew = !begins && e > e_old;       /* older tokens are rewritten */
+    const int32_t ahead = lo - base, upto = hi - base;
     const float down = pow2(-e), older = pow2(max(e_old - e, -60));
     if (threadIdx.x == 0) *scale = (uint8_t)(e + 127);
 
-    if (keys) {
-        uint8_t *out = c.k + block * c.page * D;
-        for (int32_t w = threadIdx.x; w < (hi - base - from) * oct; w += 256) {
-            const int32_t slot = from + w / oct, d0 = w % oct * 8;
-            uint2 *at = (uint2 *)(out + slot * D + d0);
-            uint2 code;
-            if (base + slot < lo) {
-                code = *at;
-                code = make_uint2(rescale4(code.x, older), rescale4(code.y, older));
-            } else {
-                const uint16_t *row = x + (s.row + base + slot - s.pos) * ld;
-                float v[8];
-                if (turn)
-                    rotate8(p, row, d0, base + slot, v);
-                else
-                    plain8(row, d0, v);
-                code = make_uint2(encode4(v[0] * down, v[1] * down, v[2] * down, v[3] * down),
-                                  encode4(v[4] * down, v[5] * down, v[6] * down, v[7] * down));
-            }
-            *at = code;
-        }
-    } else {
-        /* a thread owns four slots of one channel */
-        uint8_t *out = c.v + block * c.page * D;
-        const int32_t w0 = from >> 2, words = ((hi - base + 3) >> 2) - w0;
-        for (int32_t w = threadIdx.x; w < words * D; w += 256) {
-            const int32_t slot = (w0 + w / D) * 4, d = w % D;
-            uint32_t *at = (uint32_t *)(out + d * c.page + slot);
-            const bool whole = base + slot >= lo && base + slot + 4 <= hi;
-            uint32_t code = whole ? 0 : *at;
-            if (from == 0 && !begins && !whole) {
-                const uint32_t moved = rescale4(code, older);
-                const int32_t keep = min(max(lo - base - slot, 0), 4);
-                const uint32_t mask = keep == 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
-                code = (moved & mask) | (code & ~mask);
-            }
-            float f[4];
-            uint32_t mask = 0;
+    uint8_t *out = (keys ? c.k : c.v) + block * c.page * D;
+    const int32_t from = ahead & ~15, pitch = ((upto + 15) & ~15) - from + 4;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const int32_t w = k * 256 + (int32_t)threadIdx.x, slot = ahead + w / oct, d0 = w % oct * 8;
+        if (slot >= upto) continue;
+        const uint32_t a = encode4(v[k][0] * down, v[k][1] * down, v[k][2] * down, v[k][3] * down);
+        const uint32_t d = encode4(v[k][4] * down, v[k][5] * down, v[k][6] * down, v[k][7] * down);
+        if (keys) {
+            *(uint2 *)(out + slot * D + d0) = make_uint2(a, d);
+        } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int32_t t = base + slot + i;
-                f[i] = 0.0f;
-                if (t >= lo && t < hi) {
-                    f[i] = bf16_value(x[(s.row + t - s.pos) * ld + d]) * down;
-                    mask |= 0xFFu << (8 * i);
-                }
+                codes[(d0 + i) * pitch + slot - from] = (uint8_t)(a >> (8 * i));
+                codes[(d0 + 4 + i) * pitch + slot - from] = (uint8_t)(d >> (8 * i));
             }
-            *at = (encode4(f[0], f[1], f[2], f[3]) & mask) | (code & ~mask);
         }
     }
+    if (keys) {
+        if (grew)
+            for (int32_t w = threadIdx.x; w < ahead * oct; w += 256) {
+                uint2 *at = (uint2 *)(out + w * 8);
+                *at = make_uint2(rescale4(at->x, older), rescale4(at->y, older));
+            }
+        return;
+    }
+    __syncthreads();
+    /* 16 slots of a channel a thread; slots that are not new are read first,
+     * where any of the 16 is new or rewritten */
+    const int32_t g0 = grew ? 0 : ahead >> 4, groups = ((upto + 15) >> 4) - g0;
+    for (int32_t w = threadIdx.x; w < groups * D; w += 256) {
+        const int32_t d = w / groups, slot = (g0 + w % groups) * 16;
+        u32x4 *at = (u32x4 *)(out + d * c.page + slot);
+        u32x4 code = {0, 0, 0, 0};
+        if (slot >= from) {
+            const uint32_t *mine = (const uint32_t *)(codes + d * pitch + slot - from);
+            code = u32x4{mine[0], mine[1], mine[2], mine[3]};
+        }
+        const int32_t n0 = min(max(ahead - slot, 0), 16), n1 = min(upto - slot, 16);
+        if (n0 > 0 || n1 < 16) {
+            u32x4 old = *at;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                /* bytes [n0, n1) are new, those under n0 older */
+                const uint32_t below0 = n0 >= 4 * i + 4 ? 0xFFFFFFFFu : n0 <= 4 * i ? 0u : (1u << (8 * (n0 - 4 * i))) - 1u;
+                const uint32_t below1 = n1 >= 4 * i + 4 ? 0xFFFFFFFFu : n1 <= 4 * i ? 0u : (1u << (8 * (n1 - 4 * i))) - 1u;
+                const uint32_t was = old[i], moved = grew ? rescale4(was, older) : was;
+                const uint32_t fresh = below1 & ~below0;
+                code[i] = (code[i] & fresh) | (moved & below0) | (was & ~(fresh | below0));
+            }
+        }
+        *at = code;
+    }
 }
+
+namespace {
+
+template <int ITEMS>
+void launch_append(const KvAppendParams &p, int32_t pages_each, int32_t kv_units, int32_t q_blocks, hipStream_t stream)
+{
+    hipLaunchKernelGGL(kv_append_kernel<ITEMS>, dim3((uint32_t)(kv_units + p.c.B * q_blocks)), dim3(256), 0, stream, p, pages_each,
+                       kv_units, q_blocks);
+}
+
+} /* namespace */
 
 hipError_t launch_kv_append(const KvAppendParams &p, hipStream_t stream)
 {
@@ -274,8 +327,18 @@ hipError_t launch_kv_append(const KvAppendParams &p, hipStream_t stream)
     const int32_t kv_units = p.c.B * pages_each * p.c.H * 2;
     const int64_t per_seq = (int64_t)p.c.max_new * p.Hq * (p.D >> 3);
     const int32_t q_blocks = p.q ? (int32_t)((per_seq + 255) / 256) : 0;
-    hipLaunchKernelGGL(kv_append_kernel, dim3((uint32_t)(kv_units + p.c.B * q_blocks)), dim3(256), 0, stream, p, pages_each,
-                       kv_units, q_blocks);
+    /* octets of the most new tokens that one page can get, by 256 */
+    const int32_t items = (std::min(p.c.max_new, p.c.page) * (p.D >> 3) + 255) / 256;
+    if (items <= 1)
+        launch_append<1>(p, pages_each, kv_units, q_blocks, stream);
+    else if (items <= 2)
+        launch_append<2>(p, pages_each, kv_units, q_blocks, stream);
+    else if (items <= 4)
+        launch_append<4>(p, pages_each, kv_units, q_blocks, stream);
+    else if (items <= 8)
+        launch_append<8>(p, pages_each, kv_units, q_blocks, stream);
+    else
+        launch_append<16>(p, pages_each, kv_units, q_blocks, stream);
     return hipGetLastError();
 }
 
@@ -324,6 +387,41 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t a, uint32_t b, float s)
     return __builtin_bit_cast(bf16x8, v);
 }
 
+/* Largest of three (a NaN only if all are); fmaxf would first pass each operand
+ * through an instruction of its own to quiet NaNs. */
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+/* Largest over the four lanes of a row (lane / 16), in each of them. */
+__device__ __forceinline__ float row_max(float x)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t lo = r[0], hi = r[1];
+    const float y = max3(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi), x);
+    const uint32_t c = __builtin_bit_cast(uint32_t, y);
+    auto t = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+    const uint32_t even = t[0], odd = t[1];
+    return max3(__builtin_bit_cast(float, even), __builtin_bit_cast(float, odd), y);
+}
+
+/* Bits of the 16 tokens from t on that rows at positions lo to hi see between
+ * them. */
+__device__ __forceinline__ uint32_t seen16(const AttnParams &p, int32_t t, int32_t lo, int32_t hi)
+{
+    auto below = [](int32_t n) { return (1u << min(max(n, 0), 16)) - 1u; };
+    uint32_t bits = below(hi + 1 - t);
+    if (p.window) bits &= ~below(lo + 1 - p.window - t) | below(p.sinks - t);
+    return bits;
+}
+
+/* Four bits to the bytes of a word. */
+__device__ __forceinline__ uint32_t bytes_of(uint32_t bits) { return ((bits & 15u) * 0x00204081u & 0x01010101u) * 0xFFu; }
+
 /* Four channels of a row r: bf16 sums over the total weight, and the logarithm
  * of that weight. */
 __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, int32_t h, int32_t r, int32_t dt, int32_t q, f32x4 sum,
@@ -367,18 +465,18 @@ __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, in
  * copies, so the waits below count them all and the compiler adds none.
  */
 template <int D, int NR, int NW>
-__global__ __launch_bounds__(NW * 64) void attention_kernel(AttnParams p)
+__global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attention_kernel(AttnParams p)
 {
     constexpr int DT = D / 16, DS = D / 32, DL = D / 64, UNITS = D / 16;
-    constexpr bool QLDS = NR > 2;                  /* queries in LDS           */
     const KvParams &c = p.c;
     const int32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t lr = lane & 15, q = lane >> 4;
-    const int32_t b = blockIdx.z / c.H, h = blockIdx.z % c.H, r0 = blockIdx.y * (16 * NR);
+    const int32_t part = blockIdx.x, tile = blockIdx.y, pair = blockIdx.z;
+    const int32_t b = pair / c.H, h = pair % c.H, r0 = tile * (16 * NR);
     const Tile t = row_tile(p, b, r0, 16 * NR);
-    if (r0 >= t.rows || (int32_t)blockIdx.x >= t.parts) return;
-    const int32_t begin = (int32_t)((int64_t)t.total * blockIdx.x / t.parts);
-    const int32_t end = (int32_t)((int64_t)t.total * (blockIdx.x + 1) / t.parts);
+    if (r0 >= t.rows || part >= t.parts) return;
+    const int32_t begin = (int32_t)((int64_t)t.total * part / t.parts);
+    const int32_t end = (int32_t)((int64_t)t.total * (part + 1) / t.parts);
 
     /* LDS of a wavefront: a chunk of keys, one of values, page ids of two
      * chunks, scales of a chunk's key and value pages; behind the loop the
@@ -386,26 +484,20 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttnParams p)
     constexpr int KB = 64 * D, OWN = 2 * KB + 4 * 256;
     constexpr int JOIN = NW / 2 * NR * DT * 1024;
     __shared__ __align__(16) uint8_t store[NW * OWN > JOIN ? NW * OWN : JOIN];
-    __shared__ u32x4 queries[QLDS ? NR * DS * 64 : 1];
     __shared__ float st[NW][2][16 * NR];
     const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(store) + wave * OWN);
     uint8_t *own = store + wave * OWN;
 
     int32_t pos[NR];
-    bf16x8 qf[QLDS ? 1 : NR][DS];
+    bf16x8 qf[NR][DS];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int32_t r = min(r0 + 16 * i + lr, t.rows - 1);
         pos[i] = t.s.pos + r / p.group;
         const uint16_t *row = p.q + (int64_t)(t.s.row + r / p.group) * p.ldq + (h * p.group + r % p.group) * D + q * (D / 4);
-        if constexpr (QLDS) {
-            for (int x = wave; x < DS; x += NW) queries[(i * DS + x) * 64 + lane] = *(const u32x4 *)(row + 8 * x);
-        } else {
 #pragma unroll
-            for (int x = 0; x < DS; ++x) qf[i][x] = __builtin_bit_cast(bf16x8, *(const u32x4 *)(row + 8 * x));
-        }
+        for (int x = 0; x < DS; ++x) qf[i][x] = __builtin_bit_cast(bf16x8, *(const u32x4 *)(row + 8 * x));
     }
-    if constexpr (QLDS) __syncthreads();
 
     f32x4 o[NR][DT];
     float m[NR], l[NR];
@@ -505,15 +597,10 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttnParams p)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) kf[x] = decode8(kr[x][2 * z], kr[x][2 * z + 1], ks);
 #pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        bf16x8 f;
-                        if constexpr (QLDS)
-                            f = __builtin_bit_cast(bf16x8, queries[(i * DS + 2 * y + z) * 64 + lane]);
-                        else
-                            f = qf[i][2 * y + z];
+                    for (int i = 0; i < NR; ++i)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) s[i][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[x], f, s[i][x], 0, 0, 0);
-                    }
+                        for (int x = 0; x < 4; ++x)
+                            s[i][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[x], qf[i][2 * y + z], s[i][x], 0, 0, 0);
                 }
             }
             /* this chunk's keys are read: the next one's, and ids after that */
@@ -528,19 +615,15 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttnParams p)
             /* every row sees every token of the chunk, or masks */
             const bool inside = t0 + 63 <= t.pos_lo && (!p.window || t0 > t.pos_hi - p.window || t0 + 63 < p.sinks);
             if (!inside || __ballot(!(kok && vok)) != 0) {
-                uint32_t any[4] = {0, 0, 0, 0};   /* bytes of tokens that some row sees */
                 uint32_t mine[NR];                /* tokens that the lane's rows see    */
 #pragma unroll
-                for (int i = 0; i < NR; ++i) mine[i] = 0;
+                for (int i = 0; i < NR; ++i) mine[i] = vok ? seen16(p, vt, pos[i], pos[i]) : 0u;
+                /* those that some row sees: up to the last row's position,
+                 * within the first row's window */
+                const uint32_t some_row = vok ? seen16(p, vt, t.pos_lo, t.pos_hi) : 0u;
+                uint32_t any[4];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int32_t tk = vt + x;
-#pragma unroll
-                    for (int i = 0; i < NR; ++i)
-                        if (vok && tk <= pos[i] && (!p.window || tk > pos[i] - p.window || tk < p.sinks)) mine[i] |= 1u << x;
-                    if (vok && tk <= t.pos_hi && (!p.window || tk > t.pos_lo - p.window || tk < p.sinks))
-                        any[x >> 2] |= 0xFFu << (8 * (x & 3));
-                }
+                for (int y = 0; y < 4; ++y) any[y] = bytes_of(some_row >> (4 * y));
 #pragma unroll
                 for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -590,14 +673,20 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttnParams p)
             bf16x8 pf[NR][2];
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                float top = -__builtin_inff();
+                float top = s[i][0][0];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fmaxf(s[i][x][0], s[i][x][1]), fmaxf(s[i][x][2], s[i][x][3])));
-                top = fmaxf(top, __shfl_xor(top, 16, 64));
-                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                for (int x = 0; x < 4; ++x) {
+                    top = max3(top, s[i][x][0], s[i][x][1]);
+                    top = max3(top, s[i][x][2], s[i][x][3]);
+                }
+                top = row_max(top);
+                /* the reference of a row's weights moves only when its maximum
+                 * has passed it by a factor of 2^8: weights stay under 2^8, and
+                 * the sums are rarely touched */
                 const float now = fmaxf(m[i], top * p.scale_log2);
-                const float ref = now == -__builtin_inff() ? 0.0f : now;   /* no token seen yet */
-                if (__ballot(now != m[i]) != 0) {
+                float ref = m[i] == -__builtin_inff() ? 0.0f : m[i];       /* no token seen yet */
+                if (__ballot(now > m[i] + 8.0f) != 0) {
+                    ref = now == -__builtin_inff() ? 0.0f : now;
                     const float fade = __builtin_amdgcn_exp2f(m[i] - ref);
                     l[i] *= fade;
 #pragma unroll
@@ -691,7 +780,7 @@ __global__ __launch_bounds__(NW * 64) void attention_kernel(AttnParams p)
         __syncthreads();
     }
     if (wave != 0) return;
-    const int64_t slot = (((int64_t)blockIdx.z * p.row_tiles + blockIdx.y) * p.splits + blockIdx.x) * NR;
+    const int64_t slot = (((int64_t)pair * p.row_tiles + tile) * p.splits + part) * NR;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int32_t r = r0 + 16 * i + lr;
@@ -796,10 +885,7 @@ hipError_t launch_tile(const AttnParams &p, hipStream_t stream)
 template <int D>
 hipError_t launch_dim(const AttnParams &p, hipStream_t stream)
 {
-    constexpr int MOST = D == 256 ? 2 : 4;
-    if (p.tile_rows == 16) return launch_tile<D, 1, D == 256 ? 4 : 8>(p, stream);
-    if (p.tile_rows == 32 || MOST == 2) return launch_tile<D, 2, 4>(p, stream);
-    return launch_tile<D, MOST, 4>(p, stream);
+    return p.tile_rows == 16 ? launch_tile<D, 1, D == 256 ? 4 : 8>(p, stream) : launch_tile<D, 2, 2>(p, stream);
 }
 
 } /* namespace */

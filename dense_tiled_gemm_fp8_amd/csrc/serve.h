@@ -67,6 +67,8 @@ struct KvAppendParams {
     int64_t ldk, ldv, ldq, ldqo;  /* elements between tokens                 */
     const float *cos, *sin;       /* [positions][rot / 2] or null            */
     int32_t Hq, D, rot, interleaved;
+    int32_t whole;                /* 1: rot a multiple of 16, tables 16-byte
+                                     aligned                                */
 };
 
 struct AttnParams {

@@ -29,6 +29,11 @@ struct W4QuantParams {
     int64_t ld;                   /* elements between rows of x or y         */
     int32_t f32;                  /* x or y: 1 fp32, 0 bf16                  */
     int32_t vec;                  /* rows of x or y 16-byte aligned          */
+    /* set by the launch: octets of a row, the rows of one blockIdx.y, and the
+     * division of an octet's number by the former */
+    int32_t per_row, rows_y;
+    uint32_t magic;
+    int32_t shift;
 };
 
 struct W4GemmParams {

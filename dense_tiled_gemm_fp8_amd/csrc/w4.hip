@@ -6,14 +6,15 @@
  *          s bf16, z a byte (8 where there are no zero points)
  *   MXFP4  w[n][k] = e2m1(c[n][k]) * 2^(e[n][k / 32] - 127)
  *
- *   w4_quantize_kernel    8 consecutive elements a thread, the group's range
- *                         by shuffles among its group / 8 threads
- *   w4_dequantize_kernel  8 consecutive elements a thread
+ *   w4_quantize_kernel    8 consecutive elements a lane, the group's range by
+ *                         shuffles among its group / 8 lanes
+ *   w4_dequantize_kernel  8 consecutive elements a lane
  *   w4_gemm_kernel        y[m][n] = sum_k x[m][k] w[n][k]
  */
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <utility>
 
 #include "dma.h"
@@ -85,106 +86,185 @@ __device__ __forceinline__ uint32_t encode_e2m1(float v)
 
 } /* namespace */
 
-/* One thread for 8 elements; the group / 8 threads of a group are neighbours
- * in a wavefront. */
-__global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p)
+/* OCTETS octets (8 elements of a row) a thread, 256 apart: several, so that each
+ * thread has as many loads in flight, where a matrix has octets enough to fill the
+ * device that way.  Rows go by blockIdx.y where all of a matrix's octets would
+ * not be counted in 31 bits. */
+struct Octet {
+    int32_t n, i;                 /* row, octet of the row                    */
+    bool in;
+};
+
+template <int OCTETS>
+__device__ __forceinline__ Octet octet(const W4QuantParams &p, int k)
 {
-    const int32_t lanes = p.w.group >> 3;                 /* 4, 8 or 16        */
-    const int32_t per_row = p.w.ng * lanes;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const bool in = id < (int64_t)p.w.N * per_row;
-    const int32_t n = in ? (int32_t)(id / per_row) : 0;
-    const int32_t oct = in ? (int32_t)(id % per_row) : 0;
-    const int32_t k = oct * 8;
-    float v[8];
-    load8_row(p, n, k, v);
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        lo = fminf(lo, v[j]);
-        hi = fmaxf(hi, v[j]);
-    }
-    for (int o = lanes >> 1; o >= 1; o >>= 1) {
-        lo = fminf(lo, __shfl_xor(lo, o, 64));
-        hi = fmaxf(hi, __shfl_xor(hi, o, 64));
-    }
-    if (!in || k >= p.w.K) return;
-    const int32_t g = oct / lanes;
-    const int64_t at = (int64_t)n * p.w.ng + g;
-    const bool first = oct % lanes == 0;
-    uint32_t word = 0;
-    if (p.w.mx) {
-        const float a = fmaxf(-lo, hi);
-        const uint32_t bits = __builtin_bit_cast(uint32_t, a);
-        /* exponent of a less 2, not under 2^-127 (a's own exponent field
-         * counts from 127; a subnormal a is under 2^-126) */
-        int32_t e = (int32_t)(bits >> 23) - 2;
-        e = e < 0 ? 0 : e;
-        if (first) ((uint8_t *)p.w.scales)[at] = (uint8_t)e;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) word |= encode_e2m1(__builtin_ldexpf(v[j], 127 - e)) << (4 * j);
-    } else {
-        const float range = p.w.zeros ? hi - lo : fmaxf(-lo, hi);
-        float s = 1.0f;
-        /* the scale itself is held in 16 bits, so codes go by the rounded one */
-        if (range >= 0x1p-100f) s = (float)(__bf16)(range / (p.w.zeros ? 15.0f : 7.0f));
-        float z = 8.0f;
-        if (p.w.zeros) z = fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f);
-        if (first) {
-            ((__bf16 *)p.w.scales)[at] = (__bf16)s;
-            if (p.w.zeros) p.w.zeros[at] = (uint8_t)z;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float u = fminf(fmaxf(rintf(v[j] / s) + z, 0.0f), 15.0f);
-            word |= (k + j < p.w.K ? (uint32_t)u : 0u) << (4 * j);
-        }
-    }
-    *(uint32_t *)(p.w.codes + (int64_t)n * p.w.ldb + (k >> 1)) = word;
+    Octet o;
+    const uint32_t id = (blockIdx.x * OCTETS + (uint32_t)k) * 256u + threadIdx.x;
+    const uint32_t row = p.per_row == 1 ? id : __umulhi(id, p.magic) >> p.shift;
+    o.i = (int32_t)(id - row * (uint32_t)p.per_row);
+    const int64_t n = (int64_t)blockIdx.y * p.rows_y + row;
+    o.in = (int32_t)row < p.rows_y && n < p.w.N;
+    o.n = o.in ? (int32_t)n : 0;
+    return o;
 }
 
-__global__ __launch_bounds__(256) void w4_dequantize_kernel(W4QuantParams p)
+/* Value of the lane that CTRL names (a data-parallel-primitive control). */
+template <int CTRL>
+__device__ __forceinline__ float lane_move(float x)
 {
-    const int32_t per_row = (p.w.K + 7) >> 3;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= (int64_t)p.w.N * per_row) return;
-    const int32_t n = (int32_t)(id / per_row);
-    const int32_t k = (int32_t)(id % per_row) * 8;
-    const uint32_t word = *(const uint32_t *)(p.w.codes + (int64_t)n * p.w.ldb + (k >> 1));
-    const int64_t at = (int64_t)n * p.w.ng + k / p.w.group;
-    float v[8];
-    if (p.w.mx) {
-        const uint32_t e = ((const uint8_t *)p.w.scales)[at];
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+
+/* Smallest and largest over LANES neighbours: swaps within pairs and fours,
+ * then mirrored eights and sixteens (whose fours, eights agree by then). */
+template <int LANES>
+__device__ __forceinline__ void lane_range(float &lo, float &hi)
+{
+    lo = fminf(lo, lane_move<0xB1>(lo));
+    hi = fmaxf(hi, lane_move<0xB1>(hi));
+    lo = fminf(lo, lane_move<0x4E>(lo));
+    hi = fmaxf(hi, lane_move<0x4E>(hi));
+    if constexpr (LANES >= 8) {
+        lo = fminf(lo, lane_move<0x141>(lo));
+        hi = fmaxf(hi, lane_move<0x141>(hi));
+    }
+    if constexpr (LANES >= 16) {
+        lo = fminf(lo, lane_move<0x140>(lo));
+        hi = fmaxf(hi, lane_move<0x140>(hi));
+    }
+}
+
+/* The group / 8 threads of a group are neighbours in a wavefront.
+ *
+ * w / s is rounded to nearest from the reciprocal r of s: q0 = w r is within an
+ * ulp, and q0 + (w - q0 s) r is the quotient rounded to nearest (Markstein's
+ * theorem; the residual is exact by the fused multiply-add).  A quotient that
+ * would be subnormal rounds to the code of zero either way.  Divisions bounded
+ * the kernel before: 8192 x 8192 bf16 took 76 us, and 171 MB move. */
+template <bool MX, int LANES, int OCTETS>
+__global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p)
+{
+    constexpr int LOG2 = LANES == 4 ? 2 : LANES == 8 ? 3 : 4;
+    Octet o[OCTETS];
+    float v[OCTETS][8];
+#pragma unroll
+    for (int k = 0; k < OCTETS; ++k) {
+        o[k] = octet<OCTETS>(p, k);
+        if (o[k].in) {
+            load8_row(p, o[k].n, o[k].i * 8, v[k]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < OCTETS; ++k) {
+        float lo = 0.0f, hi = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t c = (word >> (4 * j)) & 15u, m = c & 7u;
-            /* magnitude codes 0 and 1 are 0 and 0.5, the others (2 + m % 2)
-             * times 2^(m / 2 - 2) */
-            const float mag = m < 2 ? 0.5f * (float)m : __builtin_ldexpf((float)(2 + (m & 1u)), (int)(m >> 1) - 2);
-            v[j] = e == 255 ? __builtin_nanf("") : __builtin_ldexpf(c & 8u ? -mag : mag, (int)e - 127);
+            lo = fminf(lo, v[k][j]);
+            hi = fmaxf(hi, v[k][j]);
         }
-    } else {
-        const float s = bf16_value(((const uint16_t *)p.w.scales)[at]);
-        const float z = p.w.zeros ? (float)p.w.zeros[at] : 8.0f;
+        lane_range<LANES>(lo, hi);
+        const int32_t kk = o[k].i * 8;
+        if (!o[k].in || kk >= p.w.K) continue;
+        const int64_t at = (int64_t)o[k].n * p.w.ng + (o[k].i >> LOG2);
+        const bool first = (o[k].i & (LANES - 1)) == 0;
+        uint32_t word = 0;
+        if constexpr (MX) {
+            const uint32_t bits = __builtin_bit_cast(uint32_t, fmaxf(-lo, hi));
+            /* exponent of the largest less 2, not under 2^-127 (its exponent
+             * field counts from 127; a subnormal is under 2^-126) */
+            int32_t e = (int32_t)(bits >> 23) - 2;
+            e = e < 0 ? 0 : e;
+            if (first) ((uint8_t *)p.w.scales)[at] = (uint8_t)e;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = ((float)((word >> (4 * j)) & 15u) - z) * s;
-    }
-    const int64_t o = (int64_t)n * p.ld + k;
-    if (p.vec && k + 8 <= p.w.K) {
-        if (p.f32) {
-            *(float4 *)((float *)p.y + o) = make_float4(v[0], v[1], v[2], v[3]);
-            *(float4 *)((float *)p.y + o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            for (int j = 0; j < 8; ++j) word |= encode_e2m1(__builtin_ldexpf(v[k][j], 127 - e)) << (4 * j);
         } else {
-            *(uint4 *)((uint16_t *)p.y + o) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                         pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+            const float range = p.w.zeros ? hi - lo : fmaxf(-lo, hi);
+            float s = 1.0f;
+            /* the scale itself is held in 16 bits, so codes go by the rounded one */
+            if (range >= 0x1p-100f) s = (float)(__bf16)(range / (p.w.zeros ? 15.0f : 7.0f));
+            const float r = 1.0f / s;
+            auto quotient = [&](float w) __attribute__((always_inline)) {
+                const float q0 = w * r;
+                return __builtin_fmaf(__builtin_fmaf(-q0, s, w), r, q0);
+            };
+            float z = 8.0f;
+            if (p.w.zeros) z = fminf(fmaxf(rintf(quotient(-lo)), 0.0f), 15.0f);
+            if (first) {
+                ((__bf16 *)p.w.scales)[at] = (__bf16)s;
+                if (p.w.zeros) p.w.zeros[at] = (uint8_t)z;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float u = fminf(fmaxf(rintf(quotient(v[k][j])) + z, 0.0f), 15.0f);
+                word |= (uint32_t)u << (4 * j);
+            }
+            /* elements past K read as zero, whose code is z */
+            if (kk + 8 > p.w.K) word &= (1u << (4 * (p.w.K - kk))) - 1u;
         }
-        return;
+        *(uint32_t *)(p.w.codes + (int64_t)o[k].n * p.w.ldb + (kk >> 1)) = word;
     }
-    for (int j = 0; j < 8 && k + j < p.w.K; ++j) {
-        if (p.f32)
-            ((float *)p.y)[o + j] = v[j];
-        else
-            ((__bf16 *)p.y)[o + j] = (__bf16)v[j];
+}
+
+template <int OCTETS>
+__global__ __launch_bounds__(256) void w4_dequantize_kernel(W4QuantParams p)
+{
+    Octet o[OCTETS];
+    uint32_t word[OCTETS], scale[OCTETS], zero[OCTETS];
+    const int32_t group_log2 = p.w.group == 32 ? 2 : p.w.group == 64 ? 3 : 4;   /* in octets */
+#pragma unroll
+    for (int k = 0; k < OCTETS; ++k) {
+        o[k] = octet<OCTETS>(p, k);
+        word[k] = scale[k] = 0;
+        zero[k] = 8;
+        if (!o[k].in) continue;
+        word[k] = *(const uint32_t *)(p.w.codes + (int64_t)o[k].n * p.w.ldb + o[k].i * 4);
+        const int64_t at = (int64_t)o[k].n * p.w.ng + (o[k].i >> group_log2);
+        if (p.w.mx) {
+            scale[k] = ((const uint8_t *)p.w.scales)[at];
+        } else {
+            scale[k] = ((const uint16_t *)p.w.scales)[at];
+            if (p.w.zeros) zero[k] = p.w.zeros[at];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < OCTETS; ++k) {
+        if (!o[k].in) continue;
+        const int32_t kk = o[k].i * 8;
+        float v[8];
+        if (p.w.mx) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t c = (word[k] >> (4 * j)) & 15u, m = c & 7u;
+                /* magnitude codes 0 and 1 are 0 and 0.5, the others (2 + m % 2)
+                 * times 2^(m / 2 - 2) */
+                const float mag = m < 2 ? 0.5f * (float)m : __builtin_ldexpf((float)(2 + (m & 1u)), (int)(m >> 1) - 2);
+                v[j] = scale[k] == 255 ? __builtin_nanf("") : __builtin_ldexpf(c & 8u ? -mag : mag, (int)scale[k] - 127);
+            }
+        } else {
+            const float s = bf16_value(scale[k]), z = (float)zero[k];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = ((float)((word[k] >> (4 * j)) & 15u) - z) * s;
+        }
+        const int64_t at = (int64_t)o[k].n * p.ld + kk;
+        if (p.vec && kk + 8 <= p.w.K) {
+            if (p.f32) {
+                *(float4 *)((float *)p.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+                *(float4 *)((float *)p.y + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                *(uint4 *)((uint16_t *)p.y + at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+            }
+            continue;
+        }
+        for (int j = 0; j < 8 && kk + j < p.w.K; ++j) {
+            if (p.f32)
+                ((float *)p.y)[at + j] = v[j];
+            else
+                ((__bf16 *)p.y)[at + j] = (__bf16)v[j];
+        }
     }
 }
 
@@ -553,17 +633,68 @@ __global__ __launch_bounds__(kW4AnyWaves * 64) void w4_gemm_any_kernel(W4GemmPar
     store_sums<1, 1, 4, kW4AnyWaves>(p, store, wave, lane, m0, n0, acc);
 }
 
-hipError_t launch_w4_quantize(const W4QuantParams &p, hipStream_t stream)
+namespace {
+
+/* Rows of `per_row` octets over the grid, and the division by per_row: with
+ * l = ceil(log2 per_row) and m = ceil(2^(31 + l) / per_row), floor(id / per_row)
+ * = floor(id m / 2^(31 + l)) for every id < 2^31, as m exceeds the exact
+ * quotient by less than 1 <= 2^l / per_row. */
+dim3 octet_grid(W4QuantParams &p, int64_t per_row, int octets)
 {
-    const int64_t n = (int64_t)p.w.N * p.w.ng * (p.w.group >> 3);
-    hipLaunchKernelGGL(w4_quantize_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, stream, p);
+    p.per_row = (int32_t)per_row;
+    int32_t l = 0;
+    while (((int64_t)1 << l) < per_row) ++l;
+    p.shift = l - 1;
+    p.magic = per_row == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + l)) + (uint64_t)per_row - 1) / (uint64_t)per_row);
+    const int64_t block = 256 * octets;
+    p.rows_y = (int32_t)std::min<int64_t>(p.w.N, std::max<int64_t>(1, (((int64_t)1 << 31) - block) / per_row));
+    return dim3((uint32_t)((p.rows_y * per_row + block - 1) / block), (uint32_t)((p.w.N + p.rows_y - 1) / p.rows_y));
+}
+
+/* Four octets a thread from 2^20 octets on (1024 workgroups); under that, one:
+ * 1000 x 3000 takes 6 us with one and 8 with four, 8192 x 8192 50 with four. */
+bool many(int64_t octets) { return octets >= (int64_t)1 << 20; }
+
+template <bool MX, int LANES>
+void launch_quantize_group(W4QuantParams &p, hipStream_t stream)
+{
+    const int64_t per_row = (int64_t)p.w.ng * LANES;
+    if (many(p.w.N * per_row)) {
+        const dim3 grid = octet_grid(p, per_row, 4);
+        hipLaunchKernelGGL((w4_quantize_kernel<MX, LANES, 4>), grid, dim3(256), 0, stream, p);
+    } else {
+        const dim3 grid = octet_grid(p, per_row, 1);
+        hipLaunchKernelGGL((w4_quantize_kernel<MX, LANES, 1>), grid, dim3(256), 0, stream, p);
+    }
+}
+
+} /* namespace */
+
+hipError_t launch_w4_quantize(const W4QuantParams &p0, hipStream_t stream)
+{
+    W4QuantParams p = p0;
+    if (p.w.mx)
+        launch_quantize_group<true, 4>(p, stream);
+    else if (p.w.group == 32)
+        launch_quantize_group<false, 4>(p, stream);
+    else if (p.w.group == 64)
+        launch_quantize_group<false, 8>(p, stream);
+    else
+        launch_quantize_group<false, 16>(p, stream);
     return hipGetLastError();
 }
 
-hipError_t launch_w4_dequantize(const W4QuantParams &p, hipStream_t stream)
+hipError_t launch_w4_dequantize(const W4QuantParams &p0, hipStream_t stream)
 {
-    const int64_t n = (int64_t)p.w.N * ((p.w.K + 7) >> 3);
-    hipLaunchKernelGGL(w4_dequantize_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, stream, p);
+    W4QuantParams p = p0;
+    const int64_t per_row = (p.w.K + 7) >> 3;
+    if (many(p.w.N * per_row)) {
+        const dim3 grid = octet_grid(p, per_row, 4);
+        hipLaunchKernelGGL(w4_dequantize_kernel<4>, grid, dim3(256), 0, stream, p);
+    } else {
+        const dim3 grid = octet_grid(p, per_row, 1);
+        hipLaunchKernelGGL(w4_dequantize_kernel<1>, grid, dim3(256), 0, stream, p);
+    }
     return hipGetLastError();
 }
 

@@ -256,3 +256,13 @@ def test_w4_gemm_streams_and_graph():
         torch.cuda.synchronize()
         assert torch.equal(y, want), i
     del keep
+
+
+def test_default_stream_is_the_current_one():
+    """Calls without a stream go to torch's current stream of the current device,
+    whichever it is at the call."""
+    side = torch.cuda.Stream()
+    assert g._stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert g._stream(None) == side.cuda_stream
+    assert g._stream(None) == torch.cuda.current_stream().cuda_stream != side.cuda_stream

@@ -677,6 +677,7 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     p.scale_log2 = (float)((a->scale > 0.0f ? (double)a->scale : 1.0 / sqrt((double)c.head_dim)) * 1.4426950408889634);
     p.Hq = a->q_heads;
     p.group = a->q_heads / c.heads;
+    p.by_group = divider(p.group);
     p.D = c.head_dim;
     p.window = a->window >= c.max_len ? 0 : (int32_t)a->window;
     p.sinks = (int32_t)std::min<int64_t>(a->sinks, c.max_len);

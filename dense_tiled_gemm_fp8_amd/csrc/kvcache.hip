@@ -362,8 +362,8 @@ __device__ __forceinline__ Tile row_tile(const AttnParams &p, int32_t b, int32_t
     Tile t;
     t.s = sequence(p.c, b);
     t.rows = t.s.n * p.group;
-    t.pos_lo = t.s.pos + r0 / p.group;
-    t.pos_hi = t.s.pos + min(r0 + count - 1, t.rows - 1) / p.group;
+    t.pos_lo = t.s.pos + quotient(r0, p.by_group);
+    t.pos_hi = t.s.pos + quotient(max(min(r0 + count - 1, t.rows - 1), 0), p.by_group);
     t.sink_chunks = t.first_chunk = t.total = 0;
     if (r0 < t.rows && t.pos_hi >= 0) {
         if (p.window) {
@@ -427,7 +427,7 @@ __device__ __forceinline__ uint32_t bytes_of(uint32_t bits) { return ((bits & 15
 __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, int32_t h, int32_t r, int32_t dt, int32_t q, f32x4 sum,
                                           float m, float l)
 {
-    const int32_t i = r / p.group, head = h * p.group + r % p.group;
+    const int32_t i = quotient(r, p.by_group), head = h * p.group + r - i * p.group;
     const int64_t row = t.s.row + i;
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     const float a = sum[0] * inv, b = sum[1] * inv, c = sum[2] * inv, d = sum[3] * inv;
@@ -475,15 +475,18 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
     const int32_t b = pair / c.H, h = pair % c.H, r0 = tile * (16 * NR);
     const Tile t = row_tile(p, b, r0, 16 * NR);
     if (r0 >= t.rows || part >= t.parts) return;
-    const int32_t begin = (int32_t)((int64_t)t.total * part / t.parts);
-    const int32_t end = (int32_t)((int64_t)t.total * (part + 1) / t.parts);
+    int32_t begin = 0, end = t.total;
+    if (t.parts > 1) {
+        begin = (int32_t)((int64_t)t.total * part / t.parts);
+        end = (int32_t)((int64_t)t.total * (part + 1) / t.parts);
+    }
 
     /* LDS of a wavefront: a chunk of keys, one of values, page ids of two
      * chunks, scales of a chunk's key and value pages; behind the loop the
      * sums to join */
     constexpr int KB = 64 * D, OWN = 2 * KB + 4 * 256;
-    constexpr int JOIN = NW / 2 * NR * DT * 1024;
-    __shared__ __align__(16) uint8_t store[NW * OWN > JOIN ? NW * OWN : JOIN];
+    static_assert(NR * DT * 1024 <= OWN, "sums of a wavefront take the place of its chunk");
+    __shared__ __align__(16) uint8_t store[NW * OWN];
     __shared__ float st[NW][2][16 * NR];
     const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(store) + wave * OWN);
     uint8_t *own = store + wave * OWN;
@@ -493,8 +496,9 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int32_t r = min(r0 + 16 * i + lr, t.rows - 1);
-        pos[i] = t.s.pos + r / p.group;
-        const uint16_t *row = p.q + (int64_t)(t.s.row + r / p.group) * p.ldq + (h * p.group + r % p.group) * D + q * (D / 4);
+        const int32_t token = quotient(r, p.by_group);
+        pos[i] = t.s.pos + token;
+        const uint16_t *row = p.q + (int64_t)(t.s.row + token) * p.ldq + (h * p.group + r - token * p.group) * D + q * (D / 4);
 #pragma unroll
         for (int x = 0; x < DS; ++x) qf[i][x] = __builtin_bit_cast(bf16x8, *(const u32x4 *)(row + 8 * x));
     }
@@ -738,7 +742,8 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
         wait_vmcnt<0>();                           /* the copies past the end  */
     }
 
-    /* join the wavefronts: statistics of all, then sums in halves */
+    /* join the wavefronts: statistics of all, then their sums, brought to one
+     * reference, each wavefront adding up and storing 16 channels in turn */
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         l[i] += __shfl_xor(l[i], 16, 64);
@@ -750,49 +755,41 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
     }
     __syncthreads();
     float all[NR], total[NR];
+    f32x4 *sums = (f32x4 *)store;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         all[i] = -__builtin_inff();
         total[i] = 0.0f;
+#pragma unroll
         for (int w = 0; w < NW; ++w) all[i] = fmaxf(all[i], st[w][0][16 * i + lr]);
         const float ref = all[i] == -__builtin_inff() ? 0.0f : all[i];
+#pragma unroll
         for (int w = 0; w < NW; ++w) total[i] += st[w][1][16 * i + lr] * __builtin_amdgcn_exp2f(st[w][0][16 * i + lr] - ref);
         const float f = __builtin_amdgcn_exp2f(m[i] - ref);
 #pragma unroll
-        for (int x = 0; x < DT; ++x)
+        for (int x = 0; x < DT; ++x) {
+            f32x4 v = o[i][x];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) o[i][x][y] *= f;
+            for (int y = 0; y < 4; ++y) v[y] *= f;
+            sums[((wave * NR + i) * DT + x) * 64 + lane] = v;
+        }
     }
-    f32x4 *sums = (f32x4 *)store;
-#pragma unroll
-    for (int half = NW / 2; half >= 1; half /= 2) {
-        if (wave >= half && wave < 2 * half)
-#pragma unroll
-            for (int i = 0; i < NR; ++i)
-#pragma unroll
-                for (int x = 0; x < DT; ++x) sums[(((wave - half) * NR + i) * DT + x) * 64 + lane] = o[i][x];
-        __syncthreads();
-        if (wave < half)
-#pragma unroll
-            for (int i = 0; i < NR; ++i)
-#pragma unroll
-                for (int x = 0; x < DT; ++x) o[i][x] += sums[((wave * NR + i) * DT + x) * 64 + lane];
-        __syncthreads();
-    }
-    if (wave != 0) return;
+    __syncthreads();
     const int64_t slot = (((int64_t)pair * p.row_tiles + tile) * p.splits + part) * NR;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int32_t r = r0 + 16 * i + lr;
         if (r >= t.rows) continue;
+        for (int32_t x = wave; x < DT; x += NW) {
+            f32x4 v = sums[(i * DT + x) * 64 + lane];
 #pragma unroll
-        for (int x = 0; x < DT; ++x) {
+            for (int w = 1; w < NW; ++w) v += sums[((w * NR + i) * DT + x) * 64 + lane];
             if (t.parts > 1)
-                *(f32x4 *)(p.part + ((slot + i) * DT + x) * 256 + lane * 4) = o[i][x];
+                *(f32x4 *)(p.part + ((slot + i) * DT + x) * 256 + lane * 4) = v;
             else
-                write_out(p, t, h, r, x, q, o[i][x], all[i], total[i]);
+                write_out(p, t, h, r, x, q, v, all[i], total[i]);
         }
-        if (t.parts > 1 && q == 0) {
+        if (t.parts > 1 && q == 0 && wave == 0) {
             p.stat[(slot + i) * 32 + lr] = all[i];
             p.stat[(slot + i) * 32 + 16 + lr] = total[i];
         }

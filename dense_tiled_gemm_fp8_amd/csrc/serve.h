@@ -11,6 +11,26 @@
 
 namespace g355 {
 
+/* Division of numbers under 2^31 by d: with l = ceil(log2 d) and
+ * m = ceil(2^(31 + l) / d), floor(n / d) = floor(n m / 2^(31 + l)), as m exceeds
+ * the exact quotient by less than 1 <= 2^l / d. */
+struct Divider {
+    uint32_t magic;               /* m; 0: d = 1                             */
+    int32_t shift;                /* l - 1                                   */
+};
+
+inline Divider divider(int64_t d)
+{
+    int32_t l = 0;
+    while (((int64_t)1 << l) < d) ++l;
+    return Divider{d == 1 ? 0u : (uint32_t)((((uint64_t)1 << (31 + l)) + (uint64_t)d - 1) / (uint64_t)d), l - 1};
+}
+
+__device__ __forceinline__ int32_t quotient(int32_t n, const Divider &d)
+{
+    return d.magic ? (int32_t)(__umulhi((uint32_t)n, d.magic) >> d.shift) : n;
+}
+
 /* A packed N x K matrix: two codes a byte, element 2i in the low nibble. */
 struct W4Params {
     uint8_t *codes;
@@ -29,11 +49,9 @@ struct W4QuantParams {
     int64_t ld;                   /* elements between rows of x or y         */
     int32_t f32;                  /* x or y: 1 fp32, 0 bf16                  */
     int32_t vec;                  /* rows of x or y 16-byte aligned          */
-    /* set by the launch: octets of a row, the rows of one blockIdx.y, and the
-     * division of an octet's number by the former */
+    /* set by the launch: octets of a row, the rows of one blockIdx.y */
     int32_t per_row, rows_y;
-    uint32_t magic;
-    int32_t shift;
+    Divider by_row;
 };
 
 struct W4GemmParams {
@@ -84,6 +102,7 @@ struct AttnParams {
     int64_t ldq, ldo;             /* elements between tokens                 */
     float scale_log2;             /* softmax scale times log2(e)             */
     int32_t Hq, group, D;
+    Divider by_group;
     int32_t window, sinks;        /* window 0: none                          */
     int32_t tile_rows;            /* rows a workgroup: 16, 32 or 64          */
     int32_t row_tiles;            /* of max_new * group rows                 */

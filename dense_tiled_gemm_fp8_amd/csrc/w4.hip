@@ -100,10 +100,10 @@ __device__ __forceinline__ Octet octet(const W4QuantParams &p, int k)
 {
     Octet o;
     const uint32_t id = (blockIdx.x * OCTETS + (uint32_t)k) * 256u + threadIdx.x;
-    const uint32_t row = p.per_row == 1 ? id : __umulhi(id, p.magic) >> p.shift;
-    o.i = (int32_t)(id - row * (uint32_t)p.per_row);
+    const int32_t row = quotient((int32_t)id, p.by_row);
+    o.i = (int32_t)id - row * p.per_row;
     const int64_t n = (int64_t)blockIdx.y * p.rows_y + row;
-    o.in = (int32_t)row < p.rows_y && n < p.w.N;
+    o.in = row < p.rows_y && n < p.w.N;
     o.n = o.in ? (int32_t)n : 0;
     return o;
 }
@@ -635,17 +635,11 @@ __global__ __launch_bounds__(kW4AnyWaves * 64) void w4_gemm_any_kernel(W4GemmPar
 
 namespace {
 
-/* Rows of `per_row` octets over the grid, and the division by per_row: with
- * l = ceil(log2 per_row) and m = ceil(2^(31 + l) / per_row), floor(id / per_row)
- * = floor(id m / 2^(31 + l)) for every id < 2^31, as m exceeds the exact
- * quotient by less than 1 <= 2^l / per_row. */
+/* Rows of `per_row` octets over the grid. */
 dim3 octet_grid(W4QuantParams &p, int64_t per_row, int octets)
 {
     p.per_row = (int32_t)per_row;
-    int32_t l = 0;
-    while (((int64_t)1 << l) < per_row) ++l;
-    p.shift = l - 1;
-    p.magic = per_row == 1 ? 0 : (uint32_t)((((uint64_t)1 << (31 + l)) + (uint64_t)per_row - 1) / (uint64_t)per_row);
+    p.by_row = divider(per_row);
     const int64_t block = 256 * octets;
     p.rows_y = (int32_t)std::min<int64_t>(p.w.N, std::max<int64_t>(1, (((int64_t)1 << 31) - block) / per_row));
     return dim3((uint32_t)((p.rows_y * per_row + block - 1) / block), (uint32_t)((p.w.N + p.rows_y - 1) / p.rows_y));

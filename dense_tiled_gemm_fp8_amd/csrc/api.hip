@@ -477,7 +477,8 @@ gemm355_status conv_setup(const gemm355_conv_args *c, gemm355_args &a, ConvShape
 /* ---- serving operators: argument checks ---- */
 
 const int64_t kMaxDim = (int64_t)1 << 30;
-const int64_t kMaxWide = (int64_t)1 << 24;
+const int64_t kMaxWide = (int64_t)1 << 23;
+const int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
 
 /* Extent in bytes of `rows` rows of `cols` elements, ld elements apart. */
 struct Span {
@@ -636,10 +637,10 @@ gemm355_status append_setup(const gemm355_kv_append_args *a, KvAppendParams &p)
     if (kv_meets(c, k, false) || kv_meets(c, v, false) || kv_meets(c, q, false) || kv_meets(c, cs, false) || kv_meets(c, sn, false) ||
         kv_meets(c, idx[0], false) || kv_meets(c, idx[1], false) || kv_meets(c, idx[2], false))
         return GEMM355_EINVAL;
-    const int64_t each = ((int64_t)p.c.max_new + c.page - 2) / c.page + 1;
+    /* a grid holds under 2^32 threads a dimension */
+    const int64_t kv_units = (((int64_t)p.c.max_new + c.page - 2) / c.page + 1) * c.heads * 2;
     const int64_t q_blocks = a->q ? ((int64_t)p.c.max_new * a->q_heads * (c.head_dim / 8) + 255) / 256 : 0;
-    if (each > kMaxDim / (2 * std::max<int64_t>(1, c.batch * c.heads)) || q_blocks > kMaxDim / std::max<int64_t>(1, c.batch))
-        return GEMM355_EUNSUPPORTED;
+    if (kv_units > kMaxBlocks || q_blocks > kMaxBlocks - kv_units) return GEMM355_EUNSUPPORTED;
     p.xk = (const uint16_t *)a->k;
     p.xv = (const uint16_t *)a->v;
     p.q = (const uint16_t *)a->q;
@@ -747,7 +748,7 @@ gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx, const gemm
     const gemm355_status st = check_w4(w, p.w);
     if (st != GEMM355_OK) return st;
     if (M < 0 || (out != GEMM355_SRC_F32 && out != GEMM355_SRC_BF16)) return GEMM355_EINVAL;
-    if (M > ((int64_t)1 << 19)) return GEMM355_EUNSUPPORTED;
+    if (M > ((int64_t)1 << 19) || w->N > ((int64_t)1 << 26)) return GEMM355_EUNSUPPORTED;
     const int64_t N = w->N, K = w->K, es = out == GEMM355_SRC_F32 ? 4 : 2;
     p.ldx = ldx ? ldx : K;
     p.ldy = ldy ? ldy : N;

@@ -165,9 +165,9 @@ __device__ __forceinline__ int32_t block_exponent(float a)
 
 } /* namespace */
 
-/* Work of the append: workgroups 0 .. kv_units - 1 each write the new tokens of
- * one page, head and of keys or values; those behind rotate q, 256 octets of
- * channels each.
+/* Work of the append, for sequence blockIdx.y: workgroups 0 .. kv_units - 1 each
+ * write the new tokens of one page, head and of keys or values; those behind
+ * rotate q, 256 octets of channels each.
  *
  * A page's new tokens stay in registers (ITEMS octets a thread) between finding
  * their largest magnitude and encoding them, so they are read once; values go
@@ -175,18 +175,18 @@ __device__ __forceinline__ int32_t block_exponent(float a)
  * single tokens is the chain lengths -> page id -> scale, each a load that
  * waits for the one before: tokens and tables are loaded beside it. */
 template <int ITEMS>
-__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_t pages_each, int32_t kv_units, int32_t q_blocks)
+__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_t kv_units)
 {
     const KvParams &c = p.c;
-    const int32_t D = p.D, oct = D >> 3;
+    const int32_t D = p.D, oct = D >> 3, oct_log2 = D == 64 ? 3 : D == 128 ? 4 : 5;
+    const int32_t b = blockIdx.y;
+    const Seq s = sequence(c, b);
     if ((int32_t)blockIdx.x >= kv_units) {
-        const int32_t u = (int32_t)blockIdx.x - kv_units;
-        const Seq s = sequence(c, u / q_blocks);
-        const int64_t at = (int64_t)(u % q_blocks) * 256 + threadIdx.x;
-        const int32_t per = p.Hq * oct;
-        const int32_t i = (int32_t)(at / per), rest = (int32_t)(at % per);
+        const uint32_t at = (blockIdx.x - (uint32_t)kv_units) * 256u + threadIdx.x;
+        const uint32_t row = at >> oct_log2;           /* token and head           */
+        const int32_t i = (int32_t)(row / (uint32_t)p.Hq), head = (int32_t)(row % (uint32_t)p.Hq);
+        const int32_t d0 = (int32_t)(at & (uint32_t)(oct - 1)) * 8;
         if (i >= s.n || s.pos + i < 0) return;
-        const int32_t head = rest / oct, d0 = rest % oct * 8;
         float v[8];
         const uint16_t *x = p.q + (s.row + i) * p.ldq + head * D;
         if (p.rot)
@@ -202,13 +202,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
      * to one (at most 30 more than there are tokens, of which D times as many as
      * 2048 ITEMS at most), and four bytes that spread channels over the banks */
     __shared__ __align__(16) uint8_t codes[ITEMS * 2048 + 34 * 256];
-    int32_t u = blockIdx.x;
-    const bool keys = (u & 1) == 0;
-    u >>= 1;
-    const int32_t h = u % c.H;
-    u /= c.H;
-    const int32_t j = u % pages_each, b = u / pages_each;
-    const Seq s = sequence(c, b);
+    const bool keys = (blockIdx.x & 1) == 0;
+    const int32_t h = (int32_t)(blockIdx.x >> 1) % c.H, j = (int32_t)(blockIdx.x >> 1) / c.H;
     const int32_t first = max(s.pos, 0);
     const int32_t pg = (first >> c.page_log2) + j, base = pg << c.page_log2;
     const int32_t lo = max(first, base), hi = min(s.len, base + c.page);
@@ -222,7 +217,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
     float m = 0.0f;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int32_t w = k * 256 + (int32_t)threadIdx.x, t = lo + w / oct, d0 = w % oct * 8;
+        const int32_t w = k * 256 + (int32_t)threadIdx.x, t = lo + (w >> oct_log2), d0 = (w & (oct - 1)) * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
         if (t < hi) {
@@ -258,7 +253,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
     const int32_t from = ahead & ~15, pitch = ((upto + 15) & ~15) - from + 4;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
-        const int32_t w = k * 256 + (int32_t)threadIdx.x, slot = ahead + w / oct, d0 = w % oct * 8;
+        const int32_t w = k * 256 + (int32_t)threadIdx.x, slot = ahead + (w >> oct_log2), d0 = (w & (oct - 1)) * 8;
         if (slot >= upto) continue;
         const uint32_t a = encode4(v[k][0] * down, v[k][1] * down, v[k][2] * down, v[k][3] * down);
         const uint32_t d = encode4(v[k][4] * down, v[k][5] * down, v[k][6] * down, v[k][7] * down);
@@ -312,10 +307,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
 namespace {
 
 template <int ITEMS>
-void launch_append(const KvAppendParams &p, int32_t pages_each, int32_t kv_units, int32_t q_blocks, hipStream_t stream)
+void launch_append(const KvAppendParams &p, int32_t kv_units, int32_t q_blocks, hipStream_t stream)
 {
-    hipLaunchKernelGGL(kv_append_kernel<ITEMS>, dim3((uint32_t)(kv_units + p.c.B * q_blocks)), dim3(256), 0, stream, p, pages_each,
-                       kv_units, q_blocks);
+    hipLaunchKernelGGL(kv_append_kernel<ITEMS>, dim3((uint32_t)(kv_units + q_blocks), (uint32_t)p.c.B), dim3(256), 0, stream, p, kv_units);
 }
 
 } /* namespace */
@@ -323,22 +317,20 @@ void launch_append(const KvAppendParams &p, int32_t pages_each, int32_t kv_units
 hipError_t launch_kv_append(const KvAppendParams &p, hipStream_t stream)
 {
     /* pages that max_new tokens can touch */
-    const int32_t pages_each = (p.c.max_new + p.c.page - 2) / p.c.page + 1;
-    const int32_t kv_units = p.c.B * pages_each * p.c.H * 2;
-    const int64_t per_seq = (int64_t)p.c.max_new * p.Hq * (p.D >> 3);
-    const int32_t q_blocks = p.q ? (int32_t)((per_seq + 255) / 256) : 0;
+    const int32_t kv_units = ((p.c.max_new + p.c.page - 2) / p.c.page + 1) * p.c.H * 2;
+    const int32_t q_blocks = p.q ? (int32_t)(((int64_t)p.c.max_new * p.Hq * (p.D >> 3) + 255) / 256) : 0;
     /* octets of the most new tokens that one page can get, by 256 */
     const int32_t items = (std::min(p.c.max_new, p.c.page) * (p.D >> 3) + 255) / 256;
     if (items <= 1)
-        launch_append<1>(p, pages_each, kv_units, q_blocks, stream);
+        launch_append<1>(p, kv_units, q_blocks, stream);
     else if (items <= 2)
-        launch_append<2>(p, pages_each, kv_units, q_blocks, stream);
+        launch_append<2>(p, kv_units, q_blocks, stream);
     else if (items <= 4)
-        launch_append<4>(p, pages_each, kv_units, q_blocks, stream);
+        launch_append<4>(p, kv_units, q_blocks, stream);
     else if (items <= 8)
-        launch_append<8>(p, pages_each, kv_units, q_blocks, stream);
+        launch_append<8>(p, kv_units, q_blocks, stream);
     else
-        launch_append<16>(p, pages_each, kv_units, q_blocks, stream);
+        launch_append<16>(p, kv_units, q_blocks, stream);
     return hipGetLastError();
 }
 
@@ -796,10 +788,13 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
     }
 }
 
-/* Joins the parts of 16 rows and 16 channels: four wavefronts take the parts in
- * turn, four at a time, and their sums are added in LDS in a fixed order. */
+/* Joins the parts of 16 rows and 16 channels: eight wavefronts take the parts in
+ * turn, eight at a time (all loads of 64 parts in flight at once), and their sums
+ * are added in LDS in a fixed order. */
+constexpr int kJoinWaves = 8, kJoinParts = 8;
+
 template <int D, int NR>
-__global__ __launch_bounds__(256) void attention_combine_kernel(AttnParams p)
+__global__ __launch_bounds__(kJoinWaves * 64) void attention_combine_kernel(AttnParams p)
 {
     constexpr int DT = D / 16;
     const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, q = lane >> 4;
@@ -814,21 +809,24 @@ __global__ __launch_bounds__(256) void attention_combine_kernel(AttnParams p)
     const bool in = r < t.rows;
     float m = -__builtin_inff(), l = 0.0f;
     f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int32_t k = wave; k < t.parts; k += 16) {
-        float pm[4], pl[4];
-        f32x4 v[4];
+    for (int32_t k = wave; k < t.parts; k += kJoinWaves * kJoinParts) {
+        float pm[kJoinParts], pl[kJoinParts];
+        f32x4 v[kJoinParts];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < kJoinParts; ++y) {
+            const int32_t i2 = k + kJoinWaves * y;
             pm[y] = -__builtin_inff();
             pl[y] = 0.0f;
             v[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (in && k + 4 * y < t.parts) {
-                pm[y] = stat[(int64_t)(k + 4 * y) * NR * 32];
-                pl[y] = stat[(int64_t)(k + 4 * y) * NR * 32 + 16];
-                v[y] = *(const f32x4 *)(part + (int64_t)(k + 4 * y) * NR * DT * 256);
+            if (in && i2 < t.parts) {
+                pm[y] = stat[(int64_t)i2 * NR * 32];
+                pl[y] = stat[(int64_t)i2 * NR * 32 + 16];
+                v[y] = *(const f32x4 *)(part + (int64_t)i2 * NR * DT * 256);
             }
         }
-        const float now = fmaxf(m, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
+        float now = m;
+#pragma unroll
+        for (int y = 0; y < kJoinParts; ++y) now = fmaxf(now, pm[y]);
         const float ref = now == -__builtin_inff() ? 0.0f : now;
         const float fade = __builtin_amdgcn_exp2f(m - ref);
         m = now;
@@ -836,26 +834,28 @@ __global__ __launch_bounds__(256) void attention_combine_kernel(AttnParams p)
 #pragma unroll
         for (int z = 0; z < 4; ++z) sum[z] *= fade;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < kJoinParts; ++y) {
             const float f = __builtin_amdgcn_exp2f(pm[y] - ref);
             l += f * pl[y];
 #pragma unroll
             for (int z = 0; z < 4; ++z) sum[z] += f * v[y][z];
         }
     }
-    __shared__ float st[4][2][64];
-    __shared__ f32x4 sums[4][64];
+    __shared__ float st[kJoinWaves][2][64];
+    __shared__ f32x4 sums[kJoinWaves][64];
     st[wave][0][lane] = m;
     st[wave][1][lane] = l;
     sums[wave][lane] = sum;
     __syncthreads();
     if (wave != 0 || !in) return;
-    const float all = fmaxf(fmaxf(st[0][0][lane], st[1][0][lane]), fmaxf(st[2][0][lane], st[3][0][lane]));
+    float all = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < kJoinWaves; ++w) all = fmaxf(all, st[w][0][lane]);
     const float ref = all == -__builtin_inff() ? 0.0f : all;
     float total = 0.0f;
     f32x4 out = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kJoinWaves; ++w) {
         const float f = __builtin_amdgcn_exp2f(st[w][0][lane] - ref);
         const f32x4 v = sums[w][lane];
         total += f * st[w][1][lane];
@@ -875,7 +875,7 @@ hipError_t launch_tile(const AttnParams &p, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     hipLaunchKernelGGL((attention_combine_kernel<D, NR>), dim3((uint32_t)(p.row_tiles * NR * (D / 16)), (uint32_t)(p.c.B * p.c.H)),
-                       dim3(256), 0, stream, p);
+                       dim3(kJoinWaves * 64), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -647,13 +647,13 @@ dim3 octet_grid(W4QuantParams &p, int64_t per_row, int octets)
 
 /* Four octets a thread from 2^20 octets on (1024 workgroups); under that, one:
  * 1000 x 3000 takes 6 us with one and 8 with four, 8192 x 8192 50 with four. */
-bool many(int64_t octets) { return octets >= (int64_t)1 << 20; }
+bool many_octets(int64_t octets) { return octets >= (int64_t)1 << 20; }
 
 template <bool MX, int LANES>
 void launch_quantize_group(W4QuantParams &p, hipStream_t stream)
 {
     const int64_t per_row = (int64_t)p.w.ng * LANES;
-    if (many(p.w.N * per_row)) {
+    if (many_octets(p.w.N * per_row)) {
         const dim3 grid = octet_grid(p, per_row, 4);
         hipLaunchKernelGGL((w4_quantize_kernel<MX, LANES, 4>), grid, dim3(256), 0, stream, p);
     } else {
@@ -682,7 +682,7 @@ hipError_t launch_w4_dequantize(const W4QuantParams &p0, hipStream_t stream)
 {
     W4QuantParams p = p0;
     const int64_t per_row = (p.w.K + 7) >> 3;
-    if (many(p.w.N * per_row)) {
+    if (many_octets(p.w.N * per_row)) {
         const dim3 grid = octet_grid(p, per_row, 4);
         hipLaunchKernelGGL(w4_dequantize_kernel<4>, grid, dim3(256), 0, stream, p);
     } else {
@@ -704,33 +704,45 @@ void launch_one(const W4GemmParams &p, hipStream_t stream)
     hipLaunchKernelGGL((w4_gemm_kernel<MX, GROUP, ZEROS, MT, NT, NW>), grid, dim3(NW * 64), 0, stream, q);
 }
 
+/* Rows of W a workgroup (16 NT): more of them read x less often, fewer of them
+ * make more workgroups, and about one a compute unit is wanted.  Measured on
+ * MXFP4, us (K = 4096 to 8192; the other formats have the same order):
+ *   M = 1:  N = 4096  NT 1: 4.2, 2: 4.6;     N = 8192  1: 10.9, 2: 10.3
+ *   M = 8:  N = 8192  1: 15.0, 2: 12.0, 4: 16.0;   N = 16384  2: 22.0, 4: 19.1
+ *   M = 32: N = 4096  1: 6.9, 2: 7.5;   N = 8192  1: 23.4, 2: 16.1, 4: 20.5;
+ *           N = 16384  2: 29.2, 4: 24.1
+ *   M = 64: N = 4096  1: 9.5, 2: 10.4;  N = 8192  1: 35.6, 2: 23.1 */
 template <bool MX, int GROUP, bool ZEROS>
 void launch_rows(const W4GemmParams &p, hipStream_t stream)
 {
+    const bool few = p.w.N < 8192, many = p.w.N >= 16384;
     if (!p.even) {
         const dim3 grid((uint32_t)((p.w.N + 15) / 16), (uint32_t)((p.M + 15) / 16));
         hipLaunchKernelGGL((w4_gemm_any_kernel<MX, GROUP>), grid, dim3(kW4AnyWaves * 64), 0, stream, p);
     } else if (p.M <= 4) {
-        if (p.w.N >= 8192)
-            launch_one<MX, GROUP, ZEROS, 0, 2, 8>(p, stream);
-        else
+        if (few)
             launch_one<MX, GROUP, ZEROS, 0, 1, 8>(p, stream);
+        else
+            launch_one<MX, GROUP, ZEROS, 0, 2, 8>(p, stream);
     } else if (p.M <= 16) {
-        if (p.w.N >= 16384)
-            launch_one<MX, GROUP, ZEROS, 1, 4, 4>(p, stream);
-        else if (p.w.N >= 8192)
+        if (few)
+            launch_one<MX, GROUP, ZEROS, 1, 1, 8>(p, stream);
+        else if (!many)
             launch_one<MX, GROUP, ZEROS, 1, 2, 8>(p, stream);
         else
-            launch_one<MX, GROUP, ZEROS, 1, 1, 8>(p, stream);
+            launch_one<MX, GROUP, ZEROS, 1, 4, 4>(p, stream);
     } else if (p.M <= 32) {
-        if (p.w.N >= 16384)
-            launch_one<MX, GROUP, ZEROS, 2, 4, 4>(p, stream);
-        else if (p.w.N >= 8192)
+        if (few)
+            launch_one<MX, GROUP, ZEROS, 2, 1, 4>(p, stream);
+        else if (!many)
             launch_one<MX, GROUP, ZEROS, 2, 2, 4>(p, stream);
         else
-            launch_one<MX, GROUP, ZEROS, 2, 1, 4>(p, stream);
+            launch_one<MX, GROUP, ZEROS, 2, 4, 4>(p, stream);
     } else {
-        launch_one<MX, GROUP, ZEROS, 4, 2, 4>(p, stream);
+        if (few)
+            launch_one<MX, GROUP, ZEROS, 4, 1, 4>(p, stream);
+        else
+            launch_one<MX, GROUP, ZEROS, 4, 2, 4>(p, stream);
     }
 }
 

@@ -554,7 +554,8 @@ typedef struct gemm355_w4_matrix {
  *           the even code, magnitudes above 6 to 6
  * with differences and quotients rounded to nearest in fp32, bf16() and rne()
  * to nearest with ties to even.
- *   w: device, row n at w + n * ld, K elements of `src`, finite; ld >= K.
+ *   w: device, row n at w + n * ld, K elements of `src`, finite, a group's range
+ *   under 2^128; ld >= K.
  *   q->codes, q->scales, q->zeros are written (the codes of a row up to K
  *   rounded up to 8, zeros past K).
  * One kernel, no scratch.  N or K = 0: nothing is done.
@@ -588,8 +589,8 @@ GEMM355_API gemm355_status gemm355_w4_dequantize(const gemm355_w4_matrix *q, voi
  * same bits from the same arguments every time.  M or N = 0: nothing is done;
  * K = 0: y = 0.
  * Errors: EINVAL (sizes, leading dimensions, enums, null pointers, y
- * overlapping an input), EALIGN, EUNSUPPORTED (N above 2^30, M above 2^19, ldx
- * or ldw above 2^24), EHIP.
+ * overlapping an input), EALIGN, EUNSUPPORTED (N above 2^26, M above 2^19, ldx
+ * or ldw above 2^23), EHIP.
  */
 GEMM355_API gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx,
                                const gemm355_w4_matrix *w, void *y, int64_t ldy,

@@ -689,8 +689,6 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     const int64_t tiles = std::max<int64_t>(1, c.batch * c.heads * p.row_tiles);
     int64_t seen = c.max_len;
     if (p.window) seen = std::min(seen, (int64_t)p.window + p.c.max_new + p.sinks + 128);
-    p.part_chunks = a->splits ? 4 : 16;
-    const int64_t most = std::max<int64_t>(1, (seen + 64 * p.part_chunks - 1) / (64 * p.part_chunks));
     const int32_t cus = [] {
         int n = 0;
         if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
@@ -699,8 +697,19 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
         }
         return device_cus();
     }();
-    /* workgroups that fill the device once: their LDS leaves room for one a
-     * compute unit, two where heads are small */
+    /* Wavefronts a workgroup: as many as fill a compute unit's LDS where there
+     * are at most as many workgroups as units, half of them (so that two
+     * workgroups share a unit) where there are more: heads of 128, 8 against 4
+     * wavefronts, us: 8 x 2000 tokens 15.0, 16.3; 64 x 128 tokens 13.9, 9.4;
+     * 64 x 500 19.6, 16.0.  Heads of 64 leave room for two either way. */
+    const int32_t full = p.D == 256 ? 4 : 8;
+    p.waves = p.D == 64 || tiles <= cus ? full : full / 2;
+    /* Parts: one pass of workgroups over the device, and two chunks or more a
+     * wavefront, as each part costs its share of a second kernel (one sequence,
+     * heads of 128: 8000 tokens 16.1 us so, 20.7 with four chunks or more;
+     * heads of 256: 19.8 us, 24.6 with four chunks a wavefront). */
+    p.part_chunks = a->splits ? 4 : 2 * p.waves;
+    const int64_t most = std::max<int64_t>(1, (seen + 64 * p.part_chunks - 1) / (64 * p.part_chunks));
     const int64_t want = a->splits ? a->splits : ((p.D == 64 ? 2 : 1) * (int64_t)cus + tiles - 1) / tiles;
     p.splits = (int32_t)std::min(want, most);
     const int64_t slots = tiles * p.splits;

@@ -882,7 +882,14 @@ hipError_t launch_tile(const AttnParams &p, hipStream_t stream)
 template <int D>
 hipError_t launch_dim(const AttnParams &p, hipStream_t stream)
 {
-    return p.tile_rows == 16 ? launch_tile<D, 1, D == 256 ? 4 : 8>(p, stream) : launch_tile<D, 2, 2>(p, stream);
+    if (p.tile_rows > 16) return launch_tile<D, 2, 2>(p, stream);
+    if constexpr (D <= 128)
+        if (p.waves == 8) return launch_tile<D, 1, 8>(p, stream);
+    if constexpr (D >= 128)
+        if (p.waves == 4) return launch_tile<D, 1, 4>(p, stream);
+    if constexpr (D == 256)
+        if (p.waves == 2) return launch_tile<D, 1, 2>(p, stream);
+    return hipErrorInvalidValue;
 }
 
 } /* namespace */

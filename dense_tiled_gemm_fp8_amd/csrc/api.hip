@@ -713,6 +713,7 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     const int64_t want = a->splits ? a->splits : ((p.D == 64 ? 2 : 1) * (int64_t)cus + tiles - 1) / tiles;
     p.splits = (int32_t)std::min(want, most);
     const int64_t slots = tiles * p.splits;
+    if (p.splits > 1 && slots > ((int64_t)1 << 31)) return GEMM355_EUNSUPPORTED;   /* bytes stay in 64 bits */
     bytes = p.splits > 1 ? (size_t)slots * (size_t)p.tile_rows * (size_t)(p.D + 2) * sizeof(float) : 0;
     p.part = p.stat = nullptr;
     return GEMM355_OK;
@@ -739,6 +740,11 @@ gemm355_status gemm355_w4_quantize(const void *w, int64_t ld, gemm355_src src, c
     W4QuantParams p;
     const gemm355_status st = w4_convert(q, w, ld, src, p);
     if (st != GEMM355_OK || q->N == 0 || q->K == 0) return st;
+    /* what is written lies in three places */
+    const uint64_t groups = (uint64_t)p.w.N * (uint64_t)p.w.ng;
+    const Span codes(q->codes, p.w.N, ((int64_t)p.w.K + 31) / 32 * 16, p.w.ldb, 1), zeros(q->zeros, groups);
+    const Span scales(q->scales, groups * (p.w.mx ? 1 : 2));
+    if (codes.meets(scales) || codes.meets(zeros) || scales.meets(zeros)) return GEMM355_EINVAL;
     return launch_w4_quantize(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
 }
 
@@ -820,6 +826,12 @@ gemm355_status gemm355_attention(const gemm355_attention_args *args, void *strea
         if (need && args->workspace) {
             if (args->workspace_bytes < need) return GEMM355_ENOMEM;
             if (!aligned(args->workspace, 256)) return GEMM355_EALIGN;
+            const gemm355_kv_cache &c = args->cache;
+            const Span s(args->workspace, (uint64_t)need);
+            const int64_t width = (int64_t)args->q_heads * c.head_dim;
+            if (s.meets(Span(args->q, c.tokens, width, p.ldq, 2)) || s.meets(Span(args->o, c.tokens, width, p.ldo, 2)) ||
+                s.meets(Span(args->lse, (uint64_t)(c.tokens * args->q_heads * 4))) || kv_meets(c, s, true))
+                return GEMM355_EINVAL;
             ws = args->workspace;
         } else if (need) {
             if (capturing(stream)) return GEMM355_ENOMEM;

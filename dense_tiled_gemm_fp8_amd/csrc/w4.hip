@@ -606,6 +606,13 @@ __global__ __launch_bounds__(kW4AnyWaves * 64) void w4_gemm_any_kernel(W4GemmPar
         }
         if constexpr (MX) {
             const uint32_t e = kc + 32 * q < K ? ((const uint8_t *)p.w.scales)[g0 + (kc >> 5) + q] : 127u;
+            /* codes past K are zeros: with a scale of 2^126 others might be
+             * infinities, which x = 0 does not keep out of the sums */
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t left = K - kc - 32 * q - 8 * j;
+                if (left < 8) w[j] &= left > 0 ? (1u << (4 * left)) - 1u : 0u;
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc[0][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j], decode_codes<MX>(w[j], __builtin_bit_cast(float, e << 23)),

@@ -508,7 +508,10 @@ GEMM355_API gemm355_status gemm355_conv2d_out_size(const gemm355_conv_args *args
  * product.  Weights are held in 4 bits and multiplied by bf16 rows; keys and
  * values are held in 8 bits in pages and read by attention, the other
  * workload that page "The Tensor Core" names as reducing to matrix products.
- * In the arguments below a leading dimension of 0 means packed.
+ * In the arguments below a leading dimension of 0 means packed.  Pointers and
+ * the stream belong to the current device.  A graph that a call was captured
+ * into uses the workspace it was given at every replay: graphs that may run at
+ * the same time need different ones, as calls do.
  * ---------------------------------------------------------------------------
  */
 
@@ -555,12 +558,14 @@ typedef struct gemm355_w4_matrix {
  * with differences and quotients rounded to nearest in fp32, bf16() and rne()
  * to nearest with ties to even.
  *   w: device, row n at w + n * ld, K elements of `src`, finite, a group's range
- *   under 2^128; ld >= K.
+ *   under 2^128; ld >= K.  (What is not finite gives a scale or codes without
+ *   meaning, and nothing worse.)
  *   q->codes, q->scales, q->zeros are written (the codes of a row up to K
  *   rounded up to 8, zeros past K).
  * One kernel, no scratch.  N or K = 0: nothing is done.
- * Errors: EINVAL (sizes, enums, null pointers, w overlapping what is written),
- * EALIGN, EUNSUPPORTED (N or K above 2^30, N * K above 2^40), EHIP.
+ * Errors: EINVAL (sizes, enums, null pointers, w overlapping what is written,
+ * codes, scales and zero points overlapping each other), EALIGN, EUNSUPPORTED
+ * (N or K above 2^30, N * K above 2^40), EHIP.
  */
 GEMM355_API gemm355_status gemm355_w4_quantize(const void *w, int64_t ld, gemm355_src src,
                                    const gemm355_w4_matrix *q, void *stream);
@@ -585,7 +590,8 @@ GEMM355_API gemm355_status gemm355_w4_dequantize(const gemm355_w4_matrix *q, voi
  *   x: device bf16, row m at x + m * ldx, ldx >= K, finite.
  *   y: device, row m at y + m * ldy, ldy >= N, fp32 or bf16 (`out`).
  * Sums are fp32; scales multiply the sum of a group (INT) or the element,
- * exactly (MXFP4): weights are never rounded.  One kernel, no scratch, and the
+ * exactly (MXFP4): weights are never rounded.  INT forms a group's sums of
+ * x u and of z x, which have to stay under 2^128.  One kernel, no scratch, and the
  * same bits from the same arguments every time.  M or N = 0: nothing is done;
  * K = 0: y = 0.
  * Errors: EINVAL (sizes, leading dimensions, enums, null pointers, y
@@ -698,8 +704,8 @@ GEMM355_API gemm355_status gemm355_kv_append(const gemm355_kv_append_args *args,
  * by gemm355_set_scratch_limit).  A stream that is being captured needs a
  * workspace of its own where scratch is needed (ENOMEM otherwise): a graph's
  * replays would use library-owned memory that later calls may move.
- * Errors: EINVAL (sizes, null pointers, o or lse overlapping an input or each
- * other, a scale that is negative or not finite), EALIGN, EUNSUPPORTED, ENOMEM,
+ * Errors: EINVAL (sizes, null pointers, o, lse or the workspace overlapping an
+ * input or each other, a scale that is negative or not finite), EALIGN, EUNSUPPORTED, ENOMEM,
  * EHIP.
  */
 typedef struct gemm355_attention_args {

@@ -179,3 +179,26 @@ def test_empty_steps_do_nothing():
     empty = cache(batch=0, tokens=0, table=None, lens=None, q_start=None)
     g.gemm355_kv_append(append_args(empty), stream=0)
     g.gemm355_attention(attention_args(empty), stream=0)
+
+
+def test_w4_quantize_outputs_that_overlap_are_refused():
+    x = A + 10 * STEP
+    assert status(g.gemm355_w4_quantize, x, matrix(scales=A + 64 * 128 - 2)) == g.EINVAL
+    assert status(g.gemm355_w4_quantize, x, matrix(zeros=A + 16)) == g.EINVAL
+    assert status(g.gemm355_w4_quantize, x, matrix(zeros=A + STEP + 64 * 4 * 2 - 1)) == g.EINVAL
+
+
+def test_attention_workspace_over_other_buffers_is_refused():
+    for at in (X - 256, X + STEP, X + 2 * STEP, A, A + STEP, A + 4 * STEP, A + 6 * STEP):
+        c = cache(max_len=4000)
+        assert status(g.gemm355_attention, attention_args(c, workspace=at, workspace_bytes=1 << 30, splits=4)) == g.EINVAL
+
+
+def test_attention_scratch_past_64_bits_is_refused():
+    c = cache(batch=8000, heads=8, max_len=1 << 30, table=1 << 12, table_ld=1 << 23, page=128, tokens=1 << 16, max_new=1 << 12,
+              lens=1 << 20, k=A, v=2 * A, pages=10)
+    a = attention_args(c, q_heads=8, q=4 * A, o=5 * A, lse=None, splits=1 << 30)
+    assert status(g.gemm355_attention, a) == g.EUNSUPPORTED
+    with pytest.raises(g.Gemm355Error) as e:
+        g.gemm355_attention_workspace(a)
+    assert e.value.status == g.EUNSUPPORTED

@@ -683,12 +683,7 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     p.window = a->window >= c.max_len ? 0 : (int32_t)a->window;
     p.sinks = (int32_t)std::min<int64_t>(a->sinks, c.max_len);
     const int64_t rows = (int64_t)p.c.max_new * p.group;
-    p.tile_rows = rows <= 16 ? 16 : 32;
     if (rows > (int64_t)16 * 65535) return GEMM355_EUNSUPPORTED;
-    p.row_tiles = (int32_t)((rows + p.tile_rows - 1) / p.tile_rows);
-    const int64_t tiles = std::max<int64_t>(1, c.batch * c.heads * p.row_tiles);
-    int64_t seen = c.max_len;
-    if (p.window) seen = std::min(seen, (int64_t)p.window + p.c.max_new + p.sinks + 128);
     const int32_t cus = [] {
         int n = 0;
         if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
@@ -697,18 +692,37 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
         }
         return device_cus();
     }();
-    /* Wavefronts a workgroup: as many as fill a compute unit's LDS where there
-     * are at most as many workgroups as units, half of them (so that two
-     * workgroups share a unit) where there are more: heads of 128, 8 against 4
-     * wavefronts, us: 8 x 2000 tokens 15.0, 16.3; 64 x 128 tokens 13.9, 9.4;
-     * 64 x 500 19.6, 16.0.  Heads of 64 leave room for two either way. */
-    const int32_t full = p.D == 256 ? 4 : 8;
-    p.waves = p.D == 64 || tiles <= cus ? full : full / 2;
+    /* Rows a workgroup: 16 while that makes no more workgroups than compute
+     * units (heads of 256, whose 32 rows fill the registers: two a unit), else
+     * 32, for which a chunk's codes are converted once; us with 16 and 32:
+     *   heads of 64:   128 tokens of 4 x 4 heads, 2000 held 12.0, 18.9;
+     *                  500 held, 2 x 160 of 8 x 4  11.4, 9.8
+     *   heads of 128:  16.6, 27.5;  16.7, 14.8;  4 x 512 of 4 x 4 with a window
+     *                  of 2048  96, 62
+     *   heads of 256:  300 tokens of 8 x 1 13.0, 20.3;  500 held, 2 x 160 of
+     *                  8 x 4  32.3, 26.5 */
+    const int64_t pairs = c.batch * c.heads;
+    p.tile_rows = rows <= 16 || pairs * ((rows + 15) / 16) <= (p.D == 256 ? 2 : 1) * cus ? 16 : 32;
+    p.row_tiles = (int32_t)((rows + p.tile_rows - 1) / p.tile_rows);
+    const int64_t tiles = std::max<int64_t>(1, pairs * p.row_tiles);
+    int64_t seen = c.max_len;
+    if (p.window) seen = std::min(seen, (int64_t)p.window + p.c.max_new + p.sinks + 128);
+    /* Wavefronts a workgroup of 16 rows: as many as fill a compute unit's LDS
+     * where there are at most as many workgroups as units, half of them (so that
+     * two workgroups share a unit) where there are more: heads of 128, 8 against
+     * 4 wavefronts, us: 8 x 2000 tokens 15.0, 16.3; 64 x 128 tokens 13.9, 9.4;
+     * 64 x 500 19.6, 16.0.  Heads of 64 leave room for two either way.
+     * Of 32 rows, 4 up to two workgroups a unit, else 2: 384 tokens of 8 x 4
+     * heads of 128 with 2000 held 31.1, 47.7; 4 x 512 with a window 70, 62. */
+    if (p.tile_rows == 32)
+        p.waves = p.D < 256 && tiles <= 2 * cus ? 4 : 2;
+    else
+        p.waves = (p.D == 256 ? 4 : 8) / (p.D == 64 || tiles <= cus ? 1 : 2);
     /* Parts: one pass of workgroups over the device, and two chunks or more a
      * wavefront, as each part costs its share of a second kernel (one sequence,
      * heads of 128: 8000 tokens 16.1 us so, 20.7 with four chunks or more;
      * heads of 256: 19.8 us, 24.6 with four chunks a wavefront). */
-    p.part_chunks = a->splits ? 4 : 2 * p.waves;
+    p.part_chunks = a->splits ? 4 : p.tile_rows == 32 ? 16 : 2 * p.waves;
     const int64_t most = std::max<int64_t>(1, (seen + 64 * p.part_chunks - 1) / (64 * p.part_chunks));
     const int64_t want = a->splits ? a->splits : ((p.D == 64 ? 2 : 1) * (int64_t)cus + tiles - 1) / tiles;
     p.splits = (int32_t)std::min(want, most);

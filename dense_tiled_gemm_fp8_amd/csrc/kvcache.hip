@@ -463,7 +463,9 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
     const KvParams &c = p.c;
     const int32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t lr = lane & 15, q = lane >> 4;
-    const int32_t part = blockIdx.x, tile = blockIdx.y, pair = blockIdx.z;
+    /* the last rows see the most tokens: they begin first (4096 new tokens of 32
+     * heads of 128, 262 us the other way round, 250 so) */
+    const int32_t part = blockIdx.x, tile = (int32_t)(gridDim.y - 1 - blockIdx.y), pair = blockIdx.z;
     const int32_t b = pair / c.H, h = pair % c.H, r0 = tile * (16 * NR);
     const Tile t = row_tile(p, b, r0, 16 * NR);
     if (r0 >= t.rows || part >= t.parts) return;
@@ -882,7 +884,12 @@ hipError_t launch_tile(const AttnParams &p, hipStream_t stream)
 template <int D>
 hipError_t launch_dim(const AttnParams &p, hipStream_t stream)
 {
-    if (p.tile_rows > 16) return launch_tile<D, 2, 2>(p, stream);
+    if (p.tile_rows > 16) {
+        if constexpr (D <= 128)
+            if (p.waves == 4) return launch_tile<D, 2, 4>(p, stream);
+        if (p.waves == 2) return launch_tile<D, 2, 2>(p, stream);
+        return hipErrorInvalidValue;
+    }
     if constexpr (D <= 128)
         if (p.waves == 8) return launch_tile<D, 1, 8>(p, stream);
     if constexpr (D >= 128)

@@ -104,10 +104,11 @@ struct AttnParams {
     int32_t Hq, group, D;
     Divider by_group;
     int32_t window, sinks;        /* window 0: none                          */
-    int32_t tile_rows;            /* rows a workgroup: 16, 32 or 64          */
+    int32_t tile_rows;            /* rows a workgroup: 16 or 32              */
     int32_t row_tiles;            /* of max_new * group rows                 */
-    int32_t waves;                /* wavefronts a workgroup of 16 rows: 8 (D
-                                     64, 128), 4 (D 128, 256) or 2 (D 256)  */
+    int32_t waves;                /* wavefronts a workgroup: of 16 rows 8 (D
+                                     64, 128), 4 (D 128, 256) or 2 (D 256);
+                                     of 32 rows 4 (D 64, 128) or 2          */
     int32_t splits;               /* parts of the key axis                   */
     int32_t part_chunks;          /* least 64-token chunks a part            */
     float *part;                  /* [B H row_tiles][splits][tile_rows][D]   */

@@ -179,3 +179,19 @@ def test_steps_without_a_token():
     torch.cuda.synchronize()
     assert torch.all(out == 9.0) and torch.all(o == 0) and torch.all(lse == float("-inf"))
     assert torch.all(k == 5) and torch.all(v == 5) and torch.all(ks == 120) and torch.all(vs == 120)
+
+
+@pytest.mark.parametrize("window,sinks,splits", [(0, 0, 0), (90, 5, 0), (0, 0, 3), (400, 70, 2)])
+@pytest.mark.parametrize("D,page,new", [(64, 16, 80), (128, 64, 80), (256, 32, 140), (64, 128, 262), (128, 16, 262)])
+def test_attention_prompt_chunks_of_many_rows(D, page, new, window, sinks, splits):
+    """More rows than 16 for each compute unit, at both counts of workgroups;
+    lengths that end inside a chunk, rows that the shorter sequence lacks."""
+    c = Case(350 + D + new, [700, 301], [new, new - 7], 32, 8, D, page, extra_rows=3)
+    c.table[0, 2] = -1                               # a page that nobody holds
+    q = c.rows(32, 2.0)
+    say("attention prompts", D, page, new, window, sinks, splits)
+    kw = dict(window=window, sinks=sinks)
+    o, ls = attend(c, q, splits=splits, **kw)
+    verify(c, q, o, ls, **kw)
+    o2, _ = attend(c, q, splits=splits, **kw)
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16))

@@ -711,13 +711,14 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
      * where there are at most as many workgroups as units, half of them (so that
      * two workgroups share a unit) where there are more: heads of 128, 8 against
      * 4 wavefronts, us: 8 x 2000 tokens 15.0, 16.3; 64 x 128 tokens 13.9, 9.4;
-     * 64 x 500 19.6, 16.0.  Heads of 64 leave room for two either way.
+     * 64 x 500 19.6, 16.0; but 64 x 3000 62.2, 61.5 and 64 x 8192 148.1, 153.4.
+     * Heads of 64 leave room for two either way.
      * Of 32 rows, 4 up to two workgroups a unit, else 2: 384 tokens of 8 x 4
      * heads of 128 with 2000 held 31.1, 47.7; 4 x 512 with a window 70, 62. */
     if (p.tile_rows == 32)
         p.waves = p.D < 256 && tiles <= 2 * cus ? 4 : 2;
     else
-        p.waves = (p.D == 256 ? 4 : 8) / (p.D == 64 || tiles <= cus ? 1 : 2);
+        p.waves = (p.D == 256 ? 4 : 8) / (p.D == 64 || tiles <= cus || seen > 4096 ? 1 : 2);
     /* Parts: one pass of workgroups over the device, and two chunks or more a
      * wavefront, as each part costs its share of a second kernel (one sequence,
      * heads of 128: 8000 tokens 16.1 us so, 20.7 with four chunks or more;

@@ -195,3 +195,14 @@ def test_attention_prompt_chunks_of_many_rows(D, page, new, window, sinks, split
     verify(c, q, o, ls, **kw)
     o2, _ = attend(c, q, splits=splits, **kw)
     assert torch.equal(o.view(torch.int16), o2.view(torch.int16))
+
+
+@pytest.mark.parametrize("D", (128, 256))
+def test_attention_more_workgroups_than_units_of_long_caches(D):
+    """A step whose sequences may hold more than 4096 tokens; one does."""
+    r = np.random.default_rng(D)
+    lens = [4500] + [int(n) for n in r.integers(0, 200, 39)]
+    c = Case(400 + D, lens, [1] * 40, 8, 8, D, 64, max_len=5000)
+    q = c.rows(8, 2.0)
+    o, ls = attend(c, q)
+    verify(c, q, o, ls)

@@ -173,7 +173,12 @@ __device__ __forceinline__ int32_t block_exponent(float a)
  * their largest magnitude and encoding them, so they are read once; values go
  * through LDS as codes to lie along tokens.  What takes the time of a step of
  * single tokens is the chain lengths -> page id -> scale, each a load that
- * waits for the one before: tokens and tables are loaded beside it. */
+ * waits for the one before: tokens and tables are loaded beside it.
+ *
+ * Measured: 32 sequences, one token, 32 query and 8 key heads of 128, all of a
+ * head rotated: 4.5 us, that chain.  8 x 1000 tokens of 16 and 4 heads: 16.2 us
+ * for 77 MB, 4.7 TB/s, what a large copy reaches (62 us when tokens were read
+ * twice and values written a byte at a time). */
 template <int ITEMS>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_t kv_units)
 {
@@ -455,6 +460,17 @@ __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, in
  * and the second product, its values when that product has read its own; page
  * ids come one chunk further ahead and scales with their pages, all by the same
  * copies, so the waits below count them all and the compiler adds none.
+ *
+ * Measured: 64 sequences of 4096 to 8192 tokens, 32 query and 8 key heads of 128,
+ * one token: 148 us for 811 MB, 5.5 TB/s: memory.  2 x 65536 tokens, 16 and 2
+ * heads: 13.8 us for 59 MB, 4.3 TB/s, a fill and a drain of 64-token chunks at
+ * each end, and 3.8 us for the join of its parts.  One sequence of 700 tokens, 8
+ * heads of 64: 6.9 us, the chain lengths -> page id -> codes -> two products
+ * twice over, and the join.  4 x 512 new tokens of 16 and 4 heads of 128 with a
+ * window of 2048: 53 us, 0.53 PFLOP/s; of a SIMD's cycles half go to vector
+ * instructions (conversions of codes and exponentials, in equal parts) and a
+ * quarter to matrix instructions, and two wavefronts do not hide all of each
+ * other's waits.
  */
 template <int D, int NR, int NW>
 __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attention_kernel(AttnParams p)
@@ -812,7 +828,8 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
 
 /* Joins the parts of 16 rows and 16 channels: eight wavefronts take the parts in
  * turn, eight at a time (all loads of 64 parts in flight at once), and their sums
- * are added in LDS in a fixed order. */
+ * are added in LDS in a fixed order.  Latency bounds it: 64 parts of 4 row tiles
+ * of 128 channels, 2.1 MB, in 3.8 us, as long as an empty launch. */
 constexpr int kJoinWaves = 8, kJoinParts = 8;
 
 template <int D, int NR>

@@ -86,20 +86,19 @@ __device__ __forceinline__ uint32_t encode_e2m1(float v)
 
 } /* namespace */
 
-/* OCTETS octets (8 elements of a row) a thread, 256 apart: several, so that each
- * thread has as many loads in flight, where a matrix has octets enough to fill the
- * device that way.  Rows go by blockIdx.y where all of a matrix's octets would
- * not be counted in 31 bits. */
+/* One octet (8 elements of a row) a thread.  Rows go by blockIdx.y where all of a
+ * matrix's octets would not be counted in 31 bits.  (Four octets a thread, for
+ * more loads in flight: 48.5 us against 43.6 for 8192 x 8192 bf16, 7.0 against 5.5
+ * for 1000 x 3000 fp32; the dequantiser 26.4, 26.4 and 6.0, 4.8.) */
 struct Octet {
     int32_t n, i;                 /* row, octet of the row                    */
     bool in;
 };
 
-template <int OCTETS>
-__device__ __forceinline__ Octet octet(const W4QuantParams &p, int k)
+__device__ __forceinline__ Octet octet(const W4QuantParams &p)
 {
     Octet o;
-    const uint32_t id = (blockIdx.x * OCTETS + (uint32_t)k) * 256u + threadIdx.x;
+    const uint32_t id = blockIdx.x * 256u + threadIdx.x;
     const int32_t row = quotient((int32_t)id, p.by_row);
     o.i = (int32_t)id - row * p.per_row;
     const int64_t n = (int64_t)blockIdx.y * p.rows_y + row;
@@ -139,132 +138,117 @@ __device__ __forceinline__ void lane_range(float &lo, float &hi)
  * w / s is rounded to nearest from the reciprocal r of s: q0 = w r is within an
  * ulp, and q0 + (w - q0 s) r is the quotient rounded to nearest (Markstein's
  * theorem; the residual is exact by the fused multiply-add).  A quotient that
- * would be subnormal rounds to the code of zero either way.  Divisions bounded
- * the kernel before: 8192 x 8192 bf16 took 76 us, and 171 MB move. */
-template <bool MX, int LANES, int OCTETS>
+ * would be subnormal rounds to the code of zero either way.
+ *
+ * Memory bounds it on large matrices: 8192 x 8192 bf16 to INT with groups of 64
+ * moves 171 MB in 43.6 us, 3.9 TB/s, where a large copy reaches 4.8.  On small
+ * ones the chain of a load, the range and a store does: 1000 x 3000 fp32 to MXFP4,
+ * 14 MB, in 5.2 us. */
+template <bool MX, int LANES>
 __global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p)
 {
     constexpr int LOG2 = LANES == 4 ? 2 : LANES == 8 ? 3 : 4;
-    Octet o[OCTETS];
-    float v[OCTETS][8];
+    const Octet o = octet(p);
+    float v[8];
+    if (o.in) {
+        load8_row(p, o.n, o.i * 8, v);
+    } else {
 #pragma unroll
-    for (int k = 0; k < OCTETS; ++k) {
-        o[k] = octet<OCTETS>(p, k);
-        if (o[k].in) {
-            load8_row(p, o[k].n, o[k].i * 8, v[k]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-        }
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
     }
+    float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-    for (int k = 0; k < OCTETS; ++k) {
-        float lo = 0.0f, hi = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+        lo = fminf(lo, v[j]);
+        hi = fmaxf(hi, v[j]);
+    }
+    lane_range<LANES>(lo, hi);
+    const int32_t kk = o.i * 8;
+    if (!o.in || kk >= p.w.K) return;
+    const int64_t at = (int64_t)o.n * p.w.ng + (o.i >> LOG2);
+    const bool first = (o.i & (LANES - 1)) == 0;
+    uint32_t word = 0;
+    if constexpr (MX) {
+        const uint32_t bits = __builtin_bit_cast(uint32_t, fmaxf(-lo, hi));
+        /* exponent of the largest less 2, not under 2^-127 (its exponent
+         * field counts from 127; a subnormal is under 2^-126) */
+        int32_t e = (int32_t)(bits >> 23) - 2;
+        e = e < 0 ? 0 : e;
+        if (first) ((uint8_t *)p.w.scales)[at] = (uint8_t)e;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) word |= encode_e2m1(__builtin_ldexpf(v[j], 127 - e)) << (4 * j);
+    } else {
+        const float range = p.w.zeros ? hi - lo : fmaxf(-lo, hi);
+        float s = 1.0f;
+        /* the scale itself is held in 16 bits, so codes go by the rounded one */
+        if (range >= 0x1p-100f) s = (float)(__bf16)(range / (p.w.zeros ? 15.0f : 7.0f));
+        const float r = 1.0f / s;
+        auto quotient = [&](float w) __attribute__((always_inline)) {
+            const float q0 = w * r;
+            return __builtin_fmaf(__builtin_fmaf(-q0, s, w), r, q0);
+        };
+        float z = 8.0f;
+        if (p.w.zeros) z = fminf(fmaxf(rintf(quotient(-lo)), 0.0f), 15.0f);
+        if (first) {
+            ((__bf16 *)p.w.scales)[at] = (__bf16)s;
+            if (p.w.zeros) p.w.zeros[at] = (uint8_t)z;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            lo = fminf(lo, v[k][j]);
-            hi = fmaxf(hi, v[k][j]);
+            const float u = fminf(fmaxf(rintf(quotient(v[j])) + z, 0.0f), 15.0f);
+            word |= (uint32_t)u << (4 * j);
         }
-        lane_range<LANES>(lo, hi);
-        const int32_t kk = o[k].i * 8;
-        if (!o[k].in || kk >= p.w.K) continue;
-        const int64_t at = (int64_t)o[k].n * p.w.ng + (o[k].i >> LOG2);
-        const bool first = (o[k].i & (LANES - 1)) == 0;
-        uint32_t word = 0;
-        if constexpr (MX) {
-            const uint32_t bits = __builtin_bit_cast(uint32_t, fmaxf(-lo, hi));
-            /* exponent of the largest less 2, not under 2^-127 (its exponent
-             * field counts from 127; a subnormal is under 2^-126) */
-            int32_t e = (int32_t)(bits >> 23) - 2;
-            e = e < 0 ? 0 : e;
-            if (first) ((uint8_t *)p.w.scales)[at] = (uint8_t)e;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) word |= encode_e2m1(__builtin_ldexpf(v[k][j], 127 - e)) << (4 * j);
-        } else {
-            const float range = p.w.zeros ? hi - lo : fmaxf(-lo, hi);
-            float s = 1.0f;
-            /* the scale itself is held in 16 bits, so codes go by the rounded one */
-            if (range >= 0x1p-100f) s = (float)(__bf16)(range / (p.w.zeros ? 15.0f : 7.0f));
-            const float r = 1.0f / s;
-            auto quotient = [&](float w) __attribute__((always_inline)) {
-                const float q0 = w * r;
-                return __builtin_fmaf(__builtin_fmaf(-q0, s, w), r, q0);
-            };
-            float z = 8.0f;
-            if (p.w.zeros) z = fminf(fmaxf(rintf(quotient(-lo)), 0.0f), 15.0f);
-            if (first) {
-                ((__bf16 *)p.w.scales)[at] = (__bf16)s;
-                if (p.w.zeros) p.w.zeros[at] = (uint8_t)z;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float u = fminf(fmaxf(rintf(quotient(v[k][j])) + z, 0.0f), 15.0f);
-                word |= (uint32_t)u << (4 * j);
-            }
-            /* elements past K read as zero, whose code is z */
-            if (kk + 8 > p.w.K) word &= (1u << (4 * (p.w.K - kk))) - 1u;
-        }
-        *(uint32_t *)(p.w.codes + (int64_t)o[k].n * p.w.ldb + (kk >> 1)) = word;
+        /* elements past K read as zero, whose code is z */
+        if (kk + 8 > p.w.K) word &= (1u << (4 * (p.w.K - kk))) - 1u;
     }
+    *(uint32_t *)(p.w.codes + (int64_t)o.n * p.w.ldb + (kk >> 1)) = word;
 }
 
-template <int OCTETS>
+/* 8 weights a lane from one dword of codes and their group's scale; exact in fp32
+ * (a code less a zero point has 9 bits, a scale 8), rounded once for bf16.  The
+ * store bounds it: 8192 x 8192 to bf16, 171 MB in 26 us, 6.6 TB/s with the codes
+ * still in the caches; 1000 x 3000 to fp32 4.4 us. */
 __global__ __launch_bounds__(256) void w4_dequantize_kernel(W4QuantParams p)
 {
-    Octet o[OCTETS];
-    uint32_t word[OCTETS], scale[OCTETS], zero[OCTETS];
+    const Octet o = octet(p);
+    if (!o.in) return;
     const int32_t group_log2 = p.w.group == 32 ? 2 : p.w.group == 64 ? 3 : 4;   /* in octets */
+    const uint32_t word = *(const uint32_t *)(p.w.codes + (int64_t)o.n * p.w.ldb + o.i * 4);
+    const int64_t in_group = (int64_t)o.n * p.w.ng + (o.i >> group_log2);
+    const uint32_t scale = p.w.mx ? ((const uint8_t *)p.w.scales)[in_group] : ((const uint16_t *)p.w.scales)[in_group];
+    const uint32_t zero = p.w.zeros ? p.w.zeros[in_group] : 8;
+    const int32_t kk = o.i * 8;
+    float v[8];
+    if (p.w.mx) {
 #pragma unroll
-    for (int k = 0; k < OCTETS; ++k) {
-        o[k] = octet<OCTETS>(p, k);
-        word[k] = scale[k] = 0;
-        zero[k] = 8;
-        if (!o[k].in) continue;
-        word[k] = *(const uint32_t *)(p.w.codes + (int64_t)o[k].n * p.w.ldb + o[k].i * 4);
-        const int64_t at = (int64_t)o[k].n * p.w.ng + (o[k].i >> group_log2);
-        if (p.w.mx) {
-            scale[k] = ((const uint8_t *)p.w.scales)[at];
-        } else {
-            scale[k] = ((const uint16_t *)p.w.scales)[at];
-            if (p.w.zeros) zero[k] = p.w.zeros[at];
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t c = (word >> (4 * j)) & 15u, m = c & 7u;
+            /* magnitude codes 0 and 1 are 0 and 0.5, the others (2 + m % 2)
+             * times 2^(m / 2 - 2) */
+            const float mag = m < 2 ? 0.5f * (float)m : __builtin_ldexpf((float)(2 + (m & 1u)), (int)(m >> 1) - 2);
+            v[j] = scale == 255 ? __builtin_nanf("") : __builtin_ldexpf(c & 8u ? -mag : mag, (int)scale - 127);
         }
+    } else {
+        const float s = bf16_value(scale), z = (float)zero;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = ((float)((word >> (4 * j)) & 15u) - z) * s;
     }
-#pragma unroll
-    for (int k = 0; k < OCTETS; ++k) {
-        if (!o[k].in) continue;
-        const int32_t kk = o[k].i * 8;
-        float v[8];
-        if (p.w.mx) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t c = (word[k] >> (4 * j)) & 15u, m = c & 7u;
-                /* magnitude codes 0 and 1 are 0 and 0.5, the others (2 + m % 2)
-                 * times 2^(m / 2 - 2) */
-                const float mag = m < 2 ? 0.5f * (float)m : __builtin_ldexpf((float)(2 + (m & 1u)), (int)(m >> 1) - 2);
-                v[j] = scale[k] == 255 ? __builtin_nanf("") : __builtin_ldexpf(c & 8u ? -mag : mag, (int)scale[k] - 127);
-            }
+    const int64_t at = (int64_t)o.n * p.ld + kk;
+    if (p.vec && kk + 8 <= p.w.K) {
+        if (p.f32) {
+            *(float4 *)((float *)p.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+            *(float4 *)((float *)p.y + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
         } else {
-            const float s = bf16_value(scale[k]), z = (float)zero[k];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = ((float)((word[k] >> (4 * j)) & 15u) - z) * s;
+            *(uint4 *)((uint16_t *)p.y + at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                          pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
         }
-        const int64_t at = (int64_t)o[k].n * p.ld + kk;
-        if (p.vec && kk + 8 <= p.w.K) {
-            if (p.f32) {
-                *(float4 *)((float *)p.y + at) = make_float4(v[0], v[1], v[2], v[3]);
-                *(float4 *)((float *)p.y + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-                *(uint4 *)((uint16_t *)p.y + at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-            }
-            continue;
-        }
-        for (int j = 0; j < 8 && kk + j < p.w.K; ++j) {
-            if (p.f32)
-                ((float *)p.y)[at + j] = v[j];
-            else
-                ((__bf16 *)p.y)[at + j] = (__bf16)v[j];
-        }
+        return;
+    }
+    for (int j = 0; j < 8 && kk + j < p.w.K; ++j) {
+        if (p.f32)
+            ((float *)p.y)[at + j] = v[j];
+        else
+            ((__bf16 *)p.y)[at + j] = (__bf16)v[j];
     }
 }
 
@@ -379,7 +363,8 @@ __device__ __forceinline__ void store_sums(const W4GemmParams &p, float *store, 
  * of a chunk's codes, 16 a row of x) and each wavefront reads its own copies
  * back in the matrix order.  The 16-byte units of a row are exchanged by row
  * number, which leaves the reads free of bank conflicts.  Loads in the matrix
- * order took 64 cycles each instead of 16.
+ * order took 64 cycles each instead of 16 (one token against 16384 x 8192: 45 us
+ * with them, 20 with the copies).
  *
  * A wavefront has up to four chunks in LDS, one read while the others arrive; it
  * waits for its own copies alone, so there is no barrier in the loop.
@@ -389,6 +374,13 @@ __device__ __forceinline__ void store_sums(const W4GemmParams &p, float *store, 
  * m sits in row 4m of the instruction's 16, so a lane scales one sum, not four.
  * K is a multiple of 128, rows are 16-byte aligned, scales and zero points
  * fill whole dwords.
+ *
+ * Measured: one token against 16384 x 8192 INT (groups of 64, zero points), 73 MB
+ * in 15.5 us, 4.74 TB/s, what a large copy reaches: memory.  1024 x 1024: 3.0 us,
+ * the latency of one round of copies, sums and a join.  32 tokens against
+ * 8192 x 8192 MXFP4: 11.8 us, 3.1 TB/s of codes; every workgroup of 32 rows of W
+ * reads all of x, 134 MB from the L2 beside 37 MB from memory, and x takes 8 of a
+ * chunk's 10 KB in LDS, so fewer bytes are in flight.
  */
 template <bool MX, int GROUP, bool ZEROS, int MT, int NT, int NW>
 __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
@@ -411,7 +403,7 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
     const int32_t K = p.w.K, ng = p.w.ng;
 
     /* per-lane offsets from the workgroup's first rows (64 rows stay under
-     * 2^31 bytes: K is at most 2^24) */
+     * 2^31 bytes: rows are at most 2^23 elements apart) */
     const int32_t lrow = lane >> 2, lpiece = (lane & 3) ^ (lrow >> 2);
     uint32_t code_at[NT], x_at[XL];
 #pragma unroll
@@ -571,7 +563,9 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
 
 /* The same product for what the kernel above does not take (K not a multiple of
  * 128, unaligned rows): 16 rows of W and of x a workgroup, operands loaded in
- * the matrix order, elements past K read as zero. */
+ * the matrix order, elements past K read as zero.  Latency bounds it at the sizes
+ * that are likely odd: 5 rows, 3000 x 777, 5.1 us; 1.4 MB move.  A wavefront takes
+ * every eighth chunk, so that short rows still use all eight. */
 constexpr int kW4AnyWaves = 8;
 
 template <bool MX, int GROUP>
@@ -643,30 +637,19 @@ __global__ __launch_bounds__(kW4AnyWaves * 64) void w4_gemm_any_kernel(W4GemmPar
 namespace {
 
 /* Rows of `per_row` octets over the grid. */
-dim3 octet_grid(W4QuantParams &p, int64_t per_row, int octets)
+dim3 octet_grid(W4QuantParams &p, int64_t per_row)
 {
     p.per_row = (int32_t)per_row;
     p.by_row = divider(per_row);
-    const int64_t block = 256 * octets;
-    p.rows_y = (int32_t)std::min<int64_t>(p.w.N, std::max<int64_t>(1, (((int64_t)1 << 31) - block) / per_row));
-    return dim3((uint32_t)((p.rows_y * per_row + block - 1) / block), (uint32_t)((p.w.N + p.rows_y - 1) / p.rows_y));
+    p.rows_y = (int32_t)std::min<int64_t>(p.w.N, std::max<int64_t>(1, (((int64_t)1 << 31) - 256) / per_row));
+    return dim3((uint32_t)((p.rows_y * per_row + 255) / 256), (uint32_t)((p.w.N + p.rows_y - 1) / p.rows_y));
 }
-
-/* Four octets a thread from 2^20 octets on (1024 workgroups); under that, one:
- * 1000 x 3000 takes 6 us with one and 8 with four, 8192 x 8192 50 with four. */
-bool many_octets(int64_t octets) { return octets >= (int64_t)1 << 20; }
 
 template <bool MX, int LANES>
 void launch_quantize_group(W4QuantParams &p, hipStream_t stream)
 {
-    const int64_t per_row = (int64_t)p.w.ng * LANES;
-    if (many_octets(p.w.N * per_row)) {
-        const dim3 grid = octet_grid(p, per_row, 4);
-        hipLaunchKernelGGL((w4_quantize_kernel<MX, LANES, 4>), grid, dim3(256), 0, stream, p);
-    } else {
-        const dim3 grid = octet_grid(p, per_row, 1);
-        hipLaunchKernelGGL((w4_quantize_kernel<MX, LANES, 1>), grid, dim3(256), 0, stream, p);
-    }
+    const dim3 grid = octet_grid(p, (int64_t)p.w.ng * LANES);
+    hipLaunchKernelGGL((w4_quantize_kernel<MX, LANES>), grid, dim3(256), 0, stream, p);
 }
 
 } /* namespace */
@@ -688,14 +671,8 @@ hipError_t launch_w4_quantize(const W4QuantParams &p0, hipStream_t stream)
 hipError_t launch_w4_dequantize(const W4QuantParams &p0, hipStream_t stream)
 {
     W4QuantParams p = p0;
-    const int64_t per_row = (p.w.K + 7) >> 3;
-    if (many_octets(p.w.N * per_row)) {
-        const dim3 grid = octet_grid(p, per_row, 4);
-        hipLaunchKernelGGL(w4_dequantize_kernel<4>, grid, dim3(256), 0, stream, p);
-    } else {
-        const dim3 grid = octet_grid(p, per_row, 1);
-        hipLaunchKernelGGL(w4_dequantize_kernel<1>, grid, dim3(256), 0, stream, p);
-    }
+    const dim3 grid = octet_grid(p, ((int64_t)p.w.K + 7) >> 3);
+    hipLaunchKernelGGL(w4_dequantize_kernel, grid, dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 

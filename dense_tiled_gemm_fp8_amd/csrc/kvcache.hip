@@ -176,9 +176,9 @@ __device__ __forceinline__ int32_t block_exponent(float a)
  * waits for the one before: tokens and tables are loaded beside it.
  *
  * Measured: 32 sequences, one token, 32 query and 8 key heads of 128, all of a
- * head rotated: 4.5 us, that chain.  8 x 1000 tokens of 16 and 4 heads: 16.2 us
- * for 77 MB, 4.7 TB/s, what a large copy reaches (62 us when tokens were read
- * twice and values written a byte at a time). */
+ * head rotated: 4.8 us, that chain.  8 x 1000 tokens of 16 and 4 heads: 17.6 us
+ * for 77 MB, 4.4 TB/s, where a large copy reaches 4.8 (62 us when tokens were
+ * read twice and values written a byte at a time). */
 template <int ITEMS>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_t kv_units)
 {
@@ -462,10 +462,10 @@ __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, in
  * copies, so the waits below count them all and the compiler adds none.
  *
  * Measured: 64 sequences of 4096 to 8192 tokens, 32 query and 8 key heads of 128,
- * one token: 148 us for 811 MB, 5.5 TB/s: memory.  2 x 65536 tokens, 16 and 2
- * heads: 13.8 us for 59 MB, 4.3 TB/s, a fill and a drain of 64-token chunks at
- * each end, and 3.8 us for the join of its parts.  One sequence of 700 tokens, 8
- * heads of 64: 6.9 us, the chain lengths -> page id -> codes -> two products
+ * one token: 147 us for 811 MB, 5.5 TB/s: memory.  2 x 65536 tokens, 16 and 2
+ * heads: 14.0 us for 59 MB, 4.2 TB/s, as all workgroups begin and end together,
+ * and 3.8 us for the join of their parts.  One sequence of 700 tokens, 8 heads of
+ * 64: 7.3 us, the chain lengths -> page id -> codes -> two products
  * twice over, and the join.  4 x 512 new tokens of 16 and 4 heads of 128 with a
  * window of 2048: 53 us, 0.53 PFLOP/s; of a SIMD's cycles half go to vector
  * instructions (conversions of codes and exponentials, in equal parts) and a

@@ -564,7 +564,7 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
 /* The same product for what the kernel above does not take (K not a multiple of
  * 128, unaligned rows): 16 rows of W and of x a workgroup, operands loaded in
  * the matrix order, elements past K read as zero.  Latency bounds it at the sizes
- * that are likely odd: 5 rows, 3000 x 777, 5.1 us; 1.4 MB move.  A wavefront takes
+ * that are likely odd: 5 rows, 3000 x 777, 5.4 us; 1.4 MB move.  A wavefront takes
  * every eighth chunk, so that short rows still use all eight. */
 constexpr int kW4AnyWaves = 8;
 

@@ -5,9 +5,9 @@ Products, |y - ref| <= c * A + half a step of the output type, from the order
 of the sums: a group's sum has at most 128 terms, a wavefront adds at most
 ceil(K / 128) * (128 / group) group sums, and at most 8 wavefronts are joined.  Each of
 those n = min(K, 128) + ng + 8 additions is off by at most 2^-23 (an adder that
-truncates) of sums whose magnitude is at most A = sum |x| s (16 + u + 16 + z):
-the codes enter as 16 + u, and (16 + z) sum x is taken off, which is one more
-sum of the same length.  MXFP4 has A = sum |x w| alone.  Products of small whole numbers and
+truncates) of sums whose magnitude is at most A = sum |x| s (u + z), taken here
+as sum |x| s (32 + u + z): the codes enter as u, and z sum x is taken off, which
+is one more sum of the same length.  MXFP4 has A = sum |x w| alone.  Products of small whole numbers and
 power-of-two scales are exact in every step and compared bit for bit.
 """
 import numpy as np

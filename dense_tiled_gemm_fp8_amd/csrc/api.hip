@@ -803,6 +803,7 @@ gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx, const gemm
                      groups % (p.w.zeros ? 4 : p.w.mx ? 1 : 2) == 0
                  ? 1
                  : 0;
+    p.tiny = K < 8 || groups * (p.w.mx ? 1 : 2) < 4 || (p.w.zeros && groups < 4) ? 1 : 0;
     return launch_w4_gemm(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
 }
 

@@ -64,6 +64,8 @@ struct W4GemmParams {
     int32_t even;                 /* 1: K a multiple of 128, rows of x 16-byte
                                      aligned, scales and zero points aligned
                                      and filling whole dwords              */
+    int32_t tiny;                 /* 1: K < 8, or scales or zero points of
+                                     less than a dword                      */
     uint32_t spread;              /* set by the launch: 2^32 / workgroups    */
 };
 

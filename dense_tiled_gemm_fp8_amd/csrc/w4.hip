@@ -372,8 +372,16 @@ __device__ __forceinline__ void store_sums(const W4GemmParams &p, float *store, 
  * Rows of x past M and of W past N are read as the last ones (their sums are
  * not stored), which leaves the loop without masks.  MT = 0 is for M <= 4: row
  * m sits in row 4m of the instruction's 16, so a lane scales one sum, not four.
- * K is a multiple of 128, rows are 16-byte aligned, scales and zero points
- * fill whole dwords.
+ *
+ * ODD = false: K is a multiple of 128, rows are 16-byte aligned, scales and zero
+ * points fill whole dwords.  ODD = true: any K of 8 or more and any alignment of
+ * rows, scales and zero points (the copies take any byte address).  What a chunk
+ * has past K reads as zero: whole units by an offset out of range, the unit of x
+ * that K ends in by a shift in LDS.  Scales and zero points of a dword that would
+ * pass its array's end are read from further down and shifted.  One token against
+ * 16000 x 8000 takes 19.2 us (16000 x 8064, even: 15.7; a chunk of 8000's rows lies
+ * across two lines), 32 against 8000 x 7999 17.1, where operands loaded in the
+ * matrix order took 192.
  *
  * Measured: one token against 16384 x 8192 INT (groups of 64, zero points), 73 MB
  * in 15.5 us, 4.74 TB/s, what a large copy reaches: memory.  1024 x 1024: 3.0 us,
@@ -382,7 +390,7 @@ __device__ __forceinline__ void store_sums(const W4GemmParams &p, float *store, 
  * reads all of x, 134 MB from the L2 beside 37 MB from memory, and x takes 8 of a
  * chunk's 10 KB in LDS, so fewer bytes are in flight.
  */
-template <bool MX, int GROUP, bool ZEROS, int MT, int NT, int NW>
+template <bool MX, int GROUP, bool ZEROS, int MT, int NT, int NW, bool ODD>
 __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
 {
     constexpr int RT = MT ? MT : 1;                /* row tiles                */
@@ -415,9 +423,19 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
         x_at[i] = (uint32_t)((min(m0 + row, p.M - 1) - m0) * (int32_t)p.ldx + 8 * ((lane & 15) ^ (row & 15))) * 2;
     }
     const i32x4 rc = rsrc_words(p.w.codes + (int64_t)n0 * p.w.ldb);
-    const i32x4 rs = rsrc_words((const uint8_t *)p.w.scales + (int64_t)n0 * ng * (MX ? 1 : 2));
-    const i32x4 rz = rsrc_words(ZEROS ? p.w.zeros + (int64_t)n0 * ng : p.w.codes);
+    /* ODD: a dword further down, as the last one may begin before row n0 */
+    const int32_t lead = ODD && n0 > 0 ? 4 : 0;
+    const i32x4 rs = rsrc_words((const uint8_t *)p.w.scales + ((int64_t)n0 * ng * (MX ? 1 : 2) - lead));
+    const i32x4 rz = rsrc_words(ZEROS ? p.w.zeros + ((int64_t)n0 * ng - lead) : p.w.codes);
     const i32x4 rx = rsrc_words(p.x + (int64_t)m0 * p.ldx);
+
+    /* last byte offsets that a dword of scales or zero points may be read from */
+    int32_t last_scale = 0, last_zero = 0;
+    if constexpr (ODD) {
+        const int64_t left = (int64_t)(p.w.N - n0) * ng;
+        last_scale = (int32_t)min(left * (MX ? 1 : 2) - 4 + lead, (int64_t)0x40000000);
+        last_zero = (int32_t)min(left - 4 + lead, (int64_t)0x40000000);
+    }
 
     __shared__ __align__(16) uint8_t store[NW * OWN];
     const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(store) + wave * OWN);
@@ -427,7 +445,7 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
      * neighbours in memory, and begins it at a place of the workgroup's own, so
      * that workgroups spread over the memory channels: rows are often a power
      * of two apart. */
-    const int32_t chunks = K >> 7;
+    const int32_t chunks = ODD ? (K + 127) >> 7 : K >> 7;
     const int32_t first = chunks * wave / NW;
     const int32_t count = chunks * (wave + 1) / NW - first;
     const int32_t start = (int32_t)__umulhi(blockIdx.x * p.spread, (uint32_t)count);
@@ -440,6 +458,22 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
     auto copy = [&](int32_t slot, int32_t i) __attribute__((always_inline)) {
         const uint32_t at = base + (uint32_t)slot * SLOT;
         const uint32_t ch = (uint32_t)chunk(i), kb = i < count ? ch << 6 : kOOB, kx = i < count ? ch << 8 : kOOB;
+        if constexpr (ODD) {
+            if ((int32_t)ch == chunks - 1 && i < count) {
+                /* K ends in this chunk: units past it read nothing, and the
+                 * one of x that it ends in is read up to K, eight elements
+                 * that the wait below shifts to their place */
+                const int32_t left = K - ((int32_t)ch << 7);
+                const uint32_t cb = 32 * lpiece < left ? kb : kOOB;
+                unroll<NT>([&](auto t) { dma16<t * 1024>(rc, at, code_at[t] + cb); });
+                unroll<XL>([&](auto i) {
+                    const int32_t k = 8 * ((lane & 15) ^ ((4 * i + (lane >> 4)) & 15));
+                    const uint32_t xb = k >= left ? kOOB : kx - 2 * (uint32_t)max(k + 8 - left, 0);
+                    dma16<(NT + i) * 1024>(rx, at, x_at[i] + xb);
+                });
+                return;
+            }
+        }
         unroll<NT>([&](auto t) { dma16<t * 1024>(rc, at, code_at[t] + kb); });
         unroll<XL>([&](auto i) { dma16<(NT + i) * 1024>(rx, at, x_at[i] + kx); });
     };
@@ -452,6 +486,15 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
         const int32_t ch = chunk(min(i + (lane & 3), count - 1));
         unroll<NT>([&](auto t) {
             const uint32_t si = (uint32_t)((min(n0 + 16 * t + lrow, p.w.N - 1) - n0) * ng + ch * (MX ? 4 : GC));
+            if constexpr (ODD) {
+                /* any byte address, and never past the array's end */
+                constexpr int PER = (SD + ZEROS) * 256;
+                const int32_t byte = (int32_t)(MX ? si : 2 * si) + lead;
+                dma4(rs, at + t * PER, (uint32_t)min(byte, last_scale));
+                if constexpr (SD == 2) dma4(rs, at + t * PER + 256, (uint32_t)min(byte + 4, last_scale));
+                if constexpr (ZEROS) dma4(rz, at + t * PER + SD * 256, (uint32_t)min((int32_t)si + lead, last_zero));
+                return;
+            }
             const uint32_t ks = MX ? si : 2 * si & ~3u;
             constexpr int PER = (SD + ZEROS) * 256;
             dma4(rs, at + t * PER, ks);
@@ -487,6 +530,22 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
         const uint8_t *in = own + slot * SLOT, *xin = in + NT * 1024;
         const uint8_t *sin = own + DEPTH * SLOT + (i >> 2 & 1) * QUAD + 4 * (4 * c + (i & 3));
         const int32_t ch = chunk(i);
+        const int32_t left = K - (ch << 7);            /* of K, from this chunk on */
+        if constexpr (ODD) {
+            if (left < 128 && (left & 7) != 0) {
+                constexpr int ROWS = MT ? 16 * MT : 4;
+                if (lane < ROWS) {
+                    uint16_t *at = (uint16_t *)(own + slot * SLOT + NT * 1024 + lane * 256 + (((left >> 3) ^ (lane & 15)) << 4));
+                    const int32_t by = 8 - (left & 7);
+                    uint16_t e[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) e[j] = j + by < 8 ? at[j + by] : (uint16_t)0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) at[j] = e[j];
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+        }
         uint32_t w[NT][4], sc[NT][SD], zp[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -502,7 +561,24 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
             sc[t][0] = *(const uint32_t *)st;
             if constexpr (SD == 2) sc[t][1] = *(const uint32_t *)(st + 256);
             if constexpr (ZEROS) zp[t] = *(const uint32_t *)(st + SD * 256);
-            if constexpr (MX) {
+            if constexpr (ODD) {
+                /* read from further down at the array's end */
+                const int32_t si = (min(n0 + row, p.w.N - 1) - n0) * ng + ch * (MX ? 4 : GC), byte = (MX ? si : 2 * si) + lead;
+                sc[t][0] >>= 8 * min(max(byte - last_scale, 0), 3);
+                if constexpr (SD == 2) sc[t][1] >>= 8 * min(max(byte + 4 - last_scale, 0), 3);
+                if constexpr (ZEROS) zp[t] >>= 8 * min(max(si + lead - last_zero, 0), 3);
+                if constexpr (MX) {
+                    /* codes past K are zeros, of a block past it the scale 1:
+                     * others might be infinities */
+                    sc[t][0] = 32 * q < left ? sc[t][0] >> (8 * q) & 0xFFu : 127u;
+                    if (left < 128)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int32_t n = left - 32 * q - 8 * j;
+                            if (n < 8) w[t][j] &= n > 0 ? (1u << (4 * n)) - 1u : 0u;
+                        }
+                }
+            } else if constexpr (MX) {
                 sc[t][0] = sc[t][0] >> (8 * q) & 0xFFu;
             } else if constexpr (GC < 4) {
                 /* the dword may begin before this chunk's part of it */
@@ -544,7 +620,8 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const uint32_t two = sc[t][g >> 1];
-                    const float s = __builtin_bit_cast(float, g & 1 ? two & 0xFFFF0000u : two << 16);
+                    float s = __builtin_bit_cast(float, g & 1 ? two & 0xFFFF0000u : two << 16);
+                    if (ODD && g * GROUP >= left) s = 0.0f;        /* a group past K */
                     const float z = (float)((zp[t] >> (8 * g)) & 0xFFu);
 #pragma unroll
                     for (int i2 = 0; i2 < RT; ++i2)
@@ -561,11 +638,10 @@ __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
     store_sums<NT, RT, R, NW>(p, (float *)store, wave, lane, m0, n0, acc);
 }
 
-/* The same product for what the kernel above does not take (K not a multiple of
- * 128, unaligned rows): 16 rows of W and of x a workgroup, operands loaded in
- * the matrix order, elements past K read as zero.  Latency bounds it at the sizes
- * that are likely odd: 5 rows, 3000 x 777, 5.4 us; 1.4 MB move.  A wavefront takes
- * every eighth chunk, so that short rows still use all eight. */
+/* The same product for what the kernel above does not take (K under 8, scales or
+ * zero points of less than a dword in all): 16 rows of W and of x a workgroup,
+ * operands loaded in the matrix order, elements past K read as zero.  Nothing to
+ * gain there: the launch is all it takes. */
 constexpr int kW4AnyWaves = 8;
 
 template <bool MX, int GROUP>
@@ -685,22 +761,27 @@ void launch_one(const W4GemmParams &p, hipStream_t stream)
     const dim3 grid((uint32_t)((p.w.N + 16 * NT - 1) / (16 * NT)), (uint32_t)((p.M + rows - 1) / rows));
     W4GemmParams q = p;
     q.spread = (uint32_t)(0xFFFFFFFFu / grid.x);
-    hipLaunchKernelGGL((w4_gemm_kernel<MX, GROUP, ZEROS, MT, NT, NW>), grid, dim3(NW * 64), 0, stream, q);
+    if (p.even)
+        hipLaunchKernelGGL((w4_gemm_kernel<MX, GROUP, ZEROS, MT, NT, NW, false>), grid, dim3(NW * 64), 0, stream, q);
+    else
+        hipLaunchKernelGGL((w4_gemm_kernel<MX, GROUP, ZEROS, MT, NT, NW, true>), grid, dim3(NW * 64), 0, stream, q);
 }
 
 /* Rows of W a workgroup (16 NT): more of them read x less often, fewer of them
- * make more workgroups, and about one a compute unit is wanted.  Measured on
- * MXFP4, us (K = 4096 to 8192; the other formats have the same order):
- *   M = 1:  N = 4096  NT 1: 4.2, 2: 4.6;     N = 8192  1: 10.9, 2: 10.3
- *   M = 8:  N = 8192  1: 15.0, 2: 12.0, 4: 16.0;   N = 16384  2: 22.0, 4: 19.1
- *   M = 32: N = 4096  1: 6.9, 2: 7.5;   N = 8192  1: 23.4, 2: 16.1, 4: 20.5;
- *           N = 16384  2: 29.2, 4: 24.1
- *   M = 64: N = 4096  1: 9.5, 2: 10.4;  N = 8192  1: 35.6, 2: 23.1 */
+ * make more workgroups, and one a compute unit is wanted (256 of them): 16 rows
+ * up to N = 4096, 32 up to 8192, 64 beyond (32 for M <= 4 and M > 32).  us, groups
+ * of 64 and 128 INT and MXFP4:
+ *   M = 1:  N = 4096, K = 4096   NT 1: 4.2, 2: 4.6;   N = 8000, K = 8064  1: 10.7, 2: 9.6
+ *   M = 8:  N = 5120, K = 5120   1: 9.3, 2: 7.4;   N = 8192, K = 8192  2: 12.0, 4: 16.0;
+ *           N = 9216, K = 4096   2: 11.0, 4: 9.2
+ *   M = 32: N = 4096, K = 4096   1: 6.9, 2: 7.5;   N = 8000  1: 25.0, 2: 18.3;
+ *           N = 8192  2: 16.1, 4: 20.5;   N = 9216  2: 17.1, 4: 13.0
+ *   M = 64: N = 4096, K = 4096   1: 9.5, 2: 10.4;   N = 8000  1: 40.0, 2: 30.6 */
 template <bool MX, int GROUP, bool ZEROS>
 void launch_rows(const W4GemmParams &p, hipStream_t stream)
 {
-    const bool few = p.w.N < 8192, many = p.w.N >= 16384;
-    if (!p.even) {
+    const bool few = p.w.N <= 4096, many = p.w.N > 8192;
+    if (p.tiny) {
         const dim3 grid((uint32_t)((p.w.N + 15) / 16), (uint32_t)((p.M + 15) / 16));
         hipLaunchKernelGGL((w4_gemm_any_kernel<MX, GROUP>), grid, dim3(kW4AnyWaves * 64), 0, stream, p);
     } else if (p.M <= 4) {

@@ -206,3 +206,78 @@ def test_attention_more_workgroups_than_units_of_long_caches(D):
     q = c.rows(8, 2.0)
     o, ls = attend(c, q)
     verify(c, q, o, ls)
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMS)
+@pytest.mark.parametrize("N,K", [(8200, 389), (16401, 257), (4097, 1001), (5000, 130), (48, 8321), (33, 16383), (17, 100), (3, 9), (1, 8), (19, 8)])
+def test_w4_gemm_any_k_and_row_starts(fmt, group, zeros, N, K):
+    """Every count of rows with K of any remainder, rows of x at odd starts and
+    strides, NaN behind each and codes behind K; exact, as K <= 16512 above."""
+    rng = np.random.default_rng(N + K)
+    codes, scales, z = random_matrix(rng, N, K, fmt, group, zeros)
+    scales = rng.integers(126, 129, scales.shape).astype(np.uint8) if fmt == "mxfp4" else \
+        np.exp2(rng.integers(-1, 2, scales.shape)).astype(np.float32)
+    m, keep = matrix(codes, scales, z, fmt, group, fill=15)
+    for ldx, off in ((K, 0), (K + 3, 1), (K + 8 - K % 8, 4)):
+        flat = torch.full((off + 70 * ldx,), float("nan"), dtype=torch.bfloat16)
+        rows = flat[off:].reshape(70, ldx)
+        rows[:, :K] = torch.from_numpy(rng.integers(-4, 5, (70, K)).astype(np.float32)).to(torch.bfloat16)
+        ref = rows[:, :K].double().numpy() @ w4.values(codes, scales, z, fmt, group).T
+        buf = flat.cuda()
+        for M in (1, 4, 5, 16, 17, 32, 33, 70):
+            say("w4_gemm any", fmt, group, zeros, M, N, K, ldx, off)
+            y = product(M, buf.data_ptr() + 2 * off, m, N, "f32", ldx=ldx)
+            assert np.array_equal(y.double().cpu().numpy(), ref[:M]), (M, ldx, off)
+    del keep
+
+
+@pytest.mark.parametrize("fmt,group,zeros", FORMS)
+def test_w4_gemm_scales_of_nan_stay_in_their_rows(fmt, group, zeros):
+    """A last chunk reads more scales than its row has: the next row's, here
+    NaN, have no effect.  Rows that begin at every remainder of a dword."""
+    rng = np.random.default_rng(11)
+    for K in (100, 137, 300, 451):
+        codes, scales, z = random_matrix(rng, 40, K, fmt, group, zeros)
+        scales = np.full(scales.shape, 127, np.uint8) if fmt == "mxfp4" else np.ones(scales.shape, np.float32)
+        clean = [n for n in range(40) if n % 3]
+        ref_scales = scales.copy()
+        scales[::3] = 255 if fmt == "mxfp4" else np.nan
+        m, keep = matrix(codes, scales, z, fmt, group, fill=7)
+        x = torch.from_numpy(rng.integers(-4, 5, (3, K)).astype(np.float32)).to(torch.bfloat16)
+        y = product(3, x.cuda(), m, 40, "f32").double().cpu().numpy()
+        ref = x.double().numpy() @ w4.values(codes, ref_scales, z, fmt, group).T
+        assert np.array_equal(y[:, clean], ref[:, clean]) and np.all(np.isnan(y[:, ::3])), K
+        del keep
+
+
+def test_w4_matrix_of_more_than_4_gib_and_2_31_octets():
+    """Codes, and the values they stand for, past 32-bit offsets: the last rows
+    of a matrix of 2^17 x 2^17 elements and some."""
+    N, K = (1 << 17) + 8, 1 << 17
+    c = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    s = torch.ones(N, K // 128, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(1)
+    for rows in (slice(0, 3), slice(N - 12, N)):
+        c[rows] = torch.randint(0, 256, (c[rows].shape[0], K // 2), generator=gen, dtype=torch.uint8).cuda()
+        s[rows] = 0.5
+    m = g.make_w4_matrix(N, K, c, s, None, group=128)
+    x = torch.zeros(1, K, dtype=torch.bfloat16)
+    x[0, ::1025] = 1.0
+    y = product(1, x.cuda(), m, N, "f32")
+    dense = torch.empty(N, K, dtype=torch.bfloat16, device="cuda")
+    g.gemm355_w4_dequantize(m, dense)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 3), slice(N - 12, N)):
+        codes = c[rows].cpu().numpy()
+        u = np.stack([codes & 15, codes >> 4], -1).reshape(codes.shape[0], K)
+        v = (u.astype(np.float32) - 8) * 0.5
+        assert np.array_equal(dense[rows].float().cpu().numpy(), v)
+        assert np.array_equal(y[0, rows].double().cpu().numpy(), v.astype(np.float64) @ x[0].double().numpy())
+    assert torch.all(dense[N // 2] == -8) and torch.all(y[0, N // 2] == -8 * x.double().sum().item())
+    c2, s2 = torch.full_like(c, 0x55), torch.zeros_like(s)
+    g.gemm355_w4_quantize(dense, g.make_w4_matrix(N, K, c2, s2, None, group=128))
+    torch.cuda.synchronize()
+    tail = dense[N - 12:].float().cpu().numpy()
+    codes, scales, _ = w4.quantize(tail[:, :2048], "int", 128)
+    assert np.array_equal(c2[N - 12:, :1024].cpu().numpy(), w4.pack(codes, 2048))
+    assert np.array_equal(s2[N - 12:, :16].float().cpu().numpy(), scales)

@@ -719,13 +719,14 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
         p.waves = p.D < 256 && tiles <= 2 * cus ? 4 : 2;
     else
         p.waves = (p.D == 256 ? 4 : 8) / (p.D == 64 || tiles <= cus || seen > 4096 ? 1 : 2);
-    /* Parts: one pass of workgroups over the device, and two chunks or more a
-     * wavefront, as each part costs its share of a second kernel (one sequence,
+    /* Parts: as many as stay within one pass of workgroups over the device (18 x
+     * 3000 tokens of 8 heads of 128: one part 21.7 us, two, of which the second
+     * begins when the first is done, 31.8), and two chunks or more a wavefront, as each part costs its share of a second kernel (one sequence,
      * heads of 128: 8000 tokens 16.1 us so, 20.7 with four chunks or more;
      * heads of 256: 19.8 us, 24.6 with four chunks a wavefront). */
     p.part_chunks = a->splits ? 4 : p.tile_rows == 32 ? 16 : 2 * p.waves;
     const int64_t most = std::max<int64_t>(1, (seen + 64 * p.part_chunks - 1) / (64 * p.part_chunks));
-    const int64_t want = a->splits ? a->splits : ((p.D == 64 ? 2 : 1) * (int64_t)cus + tiles - 1) / tiles;
+    const int64_t want = a->splits ? a->splits : std::max<int64_t>(1, (p.D == 64 ? 2 : 1) * (int64_t)cus / tiles);
     p.splits = (int32_t)std::min(want, most);
     const int64_t slots = tiles * p.splits;
     if (p.splits > 1 && slots > ((int64_t)1 << 31)) return GEMM355_EUNSUPPORTED;   /* bytes stay in 64 bits */

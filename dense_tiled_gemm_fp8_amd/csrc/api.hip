@@ -713,17 +713,21 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
      * 4 wavefronts, us: 8 x 2000 tokens 15.0, 16.3; 64 x 128 tokens 13.9, 9.4;
      * 64 x 500 19.6, 16.0; but 64 x 3000 62.2, 61.5 and 64 x 8192 148.1, 153.4.
      * Heads of 64 leave room for two either way.
-     * Of 32 rows, 4 up to two workgroups a unit, else 2: 384 tokens of 8 x 4
-     * heads of 128 with 2000 held 31.1, 47.7; 4 x 512 with a window 70, 62. */
+     * Of 32 rows, 4 up to three workgroups a unit (heads of 128, of which two
+     * fit: two and a half), else 2.  us with 4 and 2, heads of 128: 384 new of 8 x
+     * 4 heads, 2000 held 31.1, 47.7; 2 x 300, 3000 held 60.7, 66.8; 700 new, 2000
+     * held 50.1, 46.8; 4 x 512 with a window 70, 62; heads of 64: 700 new, 2000
+     * held 24.9, 31.8; 2 x 512, 700 held 18.7, 17.0. */
     if (p.tile_rows == 32)
-        p.waves = p.D < 256 && tiles <= 2 * cus ? 4 : 2;
+        p.waves = p.D < 256 && 2 * tiles <= (p.D == 64 ? 6 : 5) * (int64_t)cus ? 4 : 2;
     else
         p.waves = (p.D == 256 ? 4 : 8) / (p.D == 64 || tiles <= cus || seen > 4096 ? 1 : 2);
     /* Parts: as many as stay within one pass of workgroups over the device (18 x
      * 3000 tokens of 8 heads of 128: one part 21.7 us, two, of which the second
-     * begins when the first is done, 31.8), and two chunks or more a wavefront, as each part costs its share of a second kernel (one sequence,
-     * heads of 128: 8000 tokens 16.1 us so, 20.7 with four chunks or more;
-     * heads of 256: 19.8 us, 24.6 with four chunks a wavefront). */
+     * begins when the first is done, 31.8), and two chunks or more a wavefront,
+     * as each part costs its share of a second kernel (one sequence, heads of
+     * 128: 8000 tokens 16.1 us so, 20.7 with four chunks or more; heads of 256:
+     * 19.8 us, 24.6 with four chunks a wavefront). */
     p.part_chunks = a->splits ? 4 : p.tile_rows == 32 ? 16 : 2 * p.waves;
     const int64_t most = std::max<int64_t>(1, (seen + 64 * p.part_chunks - 1) / (64 * p.part_chunks));
     const int64_t want = a->splits ? a->splits : std::max<int64_t>(1, (p.D == 64 ? 2 : 1) * (int64_t)cus / tiles);

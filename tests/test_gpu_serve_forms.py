@@ -281,3 +281,13 @@ def test_w4_matrix_of_more_than_4_gib_and_2_31_octets():
     codes, scales, _ = w4.quantize(tail[:, :2048], "int", 128)
     assert np.array_equal(c2[N - 12:, :1024].cpu().numpy(), w4.pack(codes, 2048))
     assert np.array_equal(s2[N - 12:, :16].float().cpu().numpy(), scales)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 5)])
+@pytest.mark.parametrize("D,page", [(64, 32), (128, 16)])
+def test_attention_prompt_chunks_of_most_rows(D, page, window, sinks):
+    """More than three workgroups of 32 rows for each compute unit."""
+    c = Case(420 + D, [330, 262], [262, 255], 64, 8, D, page)
+    q = c.rows(64, 2.0)
+    o, ls = attend(c, q, window=window, sinks=sinks)
+    verify(c, q, o, ls, window=window, sinks=sinks)

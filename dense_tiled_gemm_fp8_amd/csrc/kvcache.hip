@@ -662,8 +662,17 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
                     for (int x = 0; x < 16; ++x) s[i][x >> 2][x & 3] = mine[i] >> x & 1u ? s[i][x >> 2][x & 3] : -__builtin_inff();
                 /* tokens that no row sees may hold anything, a NaN too, which
                  * a weight of zero would not keep out of the sums: their bytes
-                 * are cleared (a lane clears what it reads itself) */
+                 * are cleared (a lane clears what it reads itself), and so is
+                 * the scale of a block that no row sees (0 under byte 255 is a
+                 * NaN).  A value that some of the rows see is not finite, and
+                 * found as a NaN, if its code is one, if its block's scale is
+                 * (byte 255), or if it is 2^128 or more, the code of 2^k being
+                 * 8 (k + 7): bit 7 of the code plus 128 - `past`. */
                 wait_vmcnt<KEYS>();
+                uint32_t *vbyte = (uint32_t *)(own + 2 * KB + 768 + 4 * q);
+                const uint32_t byte = *vbyte, past = byte == 255 ? 0 : min((262 - byte) << 3, 0x7Fu);
+                const uint32_t add = (128 - past) * 0x01010101u;
+                if (some_row == 0 || byte == 255) *vbyte = 127;
                 u32x4 *mem = (u32x4 *)(own + KB) + lr * 4 + (q ^ (lr >> 2));
                 uint32_t nan[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -672,14 +681,16 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         v[y] &= any[y];
-                        nan[y] |= (v[y] & 0x7F7F7F7Fu) + 0x01010101u;
+                        nan[y] |= (v[y] & 0x7F7F7F7Fu) + add;
                     }
                     mem[x * 64] = v;
                 }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) nan[y] &= any[y];
                 const uint32_t some = (nan[0] | nan[1] | nan[2] | nan[3]) & 0x80808080u;
                 if (__ballot(some != 0) != 0) {
-                    /* a NaN that some of the rows see: out of the values, and
-                     * into the scores of those rows */
+                    /* what is not finite and seen by some of the rows: out of
+                     * the values, and a NaN into the scores of those rows */
                     uint32_t tok = 0;
 #pragma unroll
                     for (int x = 0; x < 16; ++x) tok |= (nan[x >> 2] >> (8 * (x & 3) + 7) & 1u) << x;

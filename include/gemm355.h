@@ -607,7 +607,10 @@ GEMM355_API gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx
  * E8M0 scale 2^(byte - 127) for each page and head (block scaling as in the
  * MX dtypes, the block being a page's tokens of one head), and the step that
  * runs on it.  Sequence b holds lens[b] tokens, the step's new ones included;
- * its token t is slot t % page of page table[b][t / page].  Its new tokens are
+ * its token t is slot t % page of page table[b][t / page].  As elsewhere byte
+ * 255 of a scale makes its block NaN and a held value of 2^128 or more is an
+ * infinity (the append writes one for an infinity and for the largest bf16
+ * values, which round up to 2^128).  Its new tokens are
  * rows q_start[b] .. q_start[b + 1] - 1 of the step's tensors and the last of
  * the sequence: row q_start[b] + i has position
  * lens[b] - (q_start[b + 1] - q_start[b]) + i.
@@ -689,13 +692,15 @@ GEMM355_API gemm355_status gemm355_kv_append(const gemm355_kv_append_args *args,
  * 0: all of them):
  *     o = sum_t softmax_t(scale * q . k_t) v_t,  lse = log sum_t exp(scale * q . k_t).
  * A row that sees nothing gets o = 0 and lse = -infinity.  What a row does not
- * see has no effect on it, whatever it holds; a NaN in a value that a row sees
- * makes that row NaN, in that channel at least.
+ * see has no effect on it, whatever it holds, scales included; a NaN or an
+ * infinity in a value that a row sees makes that row not finite, in that
+ * channel at least.
  *   q, o: device bf16, row r head j at q + r * ldq + j * head_dim, rows 16-byte
  *   aligned (pointers EALIGN, ld* multiples of 8 EINVAL); o is written.
  *   lse: device fp32 [tokens][q_heads], written, or NULL.
  * Products and statistics are fp32; the softmax weights enter the second
- * product as bf16.
+ * product as bf16, and its sums, of values times weights of up to 2^8 before the
+ * division by their total, have to stay under 2^128.
  * The key axis is split into `splits` parts where there are few rows (0:
  * chosen from the sizes; at most one part per 256 tokens); parts go through
  * scratch and a second kernel, in a fixed order, so the same arguments give

@@ -1,0 +1,145 @@
+"""The ends of the paged 8-bit cache on the GPU: block scales of any byte, held
+values past the largest finite one, what hides them, and rows of one tile that
+must not feel each other.  Appended bytes are compared with the oracle bit for
+bit, attention by the bound of test_gpu_kvcache.py where a row is finite; rows
+that see none of what changed are compared with the unchanged cache bit for
+bit.
+"""
+import numpy as np
+import pytest
+import torch
+
+from dense_tiled_gemm_fp8_amd import gemm355 as g
+from oracle import kvcache as ok
+from tests.gpu_helpers import say
+from tests.test_gpu_kvcache import Case, attend, run_append, verify
+
+pytestmark = pytest.mark.gpu
+
+
+def free_page_0(c):
+    """Gives page 0 to nobody: whoever has it gets a page that is not in use."""
+    held = [-(-n // c.page) for n in c.lens]
+    used = {int(c.table[b, j]) for b in range(len(c.lens)) for j in range(held[b])}
+    spare = next(i for i in range(c.pages) if i not in used)
+    for b in range(len(c.lens)):
+        for j in range(held[b]):
+            if c.table[b, j] == 0:
+                c.table[b, j] = spare
+                for a in (c.k, c.v, c.ks, c.vs):
+                    a[spare] = a[0]
+    c.k[0], c.v[0] = 0x7F, 0x7F
+    return c
+
+
+def same_bits(a, b, rows):
+    rows = torch.from_numpy(rows)
+    return torch.equal(a.cpu().view(torch.int16)[rows], b.cpu().view(torch.int16)[rows])
+
+
+def positions(c):
+    """Sequence and position of each row."""
+    s = c.step()
+    at = np.full((c.tokens, 2), -1)
+    for b in range(s.batch):
+        for i in range(s.new[b]):
+            at[s.row[b] + i] = b, s.len[b] - s.new[b] + i
+    return at
+
+
+# lens, new rows, Hq, H, D, page: one row, few rows, prompts of both counts of rows a workgroup
+FORMS = [([300, 130], [1, 1], 4, 2, 64, 16), ([300, 130], [20, 7], 4, 2, 128, 16), ([300, 130], [20, 3], 4, 2, 256, 16),
+         ([400, 330], [134, 130], 32, 8, 64, 32), ([400, 330], [134, 130], 32, 8, 128, 16), ([400, 330], [134, 130], 32, 8, 256, 32)]
+
+
+@pytest.mark.parametrize("splits", (0, 2))
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_scales_of_hidden_pages_have_no_effect(i, splits):
+    """Tokens without a page, where nothing of page 0 may show; pages before the
+    window, in a chunk with pages that are seen."""
+    lens, news, Hq, H, D, page = FORMS[i]
+    say("hidden scales", FORMS[i], splits)
+    c = free_page_0(Case(500 + i, lens, news, Hq, H, D, page))
+    q = c.rows(Hq, 2.0)
+    c.table[0, 3], c.table[0, 5], c.table[1, 1] = -1, c.pages, -(1 << 31)
+    for byte in (255, 254):
+        c.ks[0], c.vs[0] = byte, byte
+        o, ls = attend(c, q, splits=splits)
+        verify(c, q, o, ls)
+    c = Case(520 + i, lens, news, Hq, H, D, page)
+    q = c.rows(Hq, 2.0)
+    # the first row's window begins with the last page of a 64-token chunk
+    window = next(w for w in range(20, 100) if (lens[0] - news[0] - w + 1) % 64 == 64 - page)
+    want, wl = attend(c, q, window=window, splits=splits)
+    verify(c, q, want, wl, window=window)
+    for b in range(2):
+        for j in range(max(0, lens[b] - news[b] - window + 1) // page):
+            c.ks[c.table[b, j]], c.vs[c.table[b, j]] = 255, 255
+    o, ls = attend(c, q, window=window, splits=splits)
+    assert same_bits(o, want, np.arange(c.tokens)) and torch.equal(ls, wl)
+
+
+@pytest.mark.parametrize("splits", (0, 2))
+@pytest.mark.parametrize("which", ("k", "v"))
+@pytest.mark.parametrize("i", range(1, len(FORMS)))
+def test_a_nan_block_reaches_the_rows_that_see_it_alone(i, which, splits):
+    lens, news, Hq, H, D, page = FORMS[i]
+    say("NaN block", FORMS[i], which, splits)
+    c = Case(540 + i, lens, news, Hq, H, D, page)
+    q = c.rows(Hq, 2.0)
+    want, wl = attend(c, q, splits=splits)
+    p0 = lens[0] - news[0]
+    at = -(-(p0 + 3) // page) * page                     # a page that begins between two rows
+    if at >= lens[0]:
+        at = p0 // page * page
+    head = 1
+    (c.ks if which == "k" else c.vs)[c.table[0, at // page], head] = 255
+    o, ls = attend(c, q, splits=splits)
+    pos = positions(c)
+    sees = (pos[:, 0] == 0) & (pos[:, 1] >= at)
+    assert sees.any()
+    group = Hq // H
+    mine = slice(head * group, (head + 1) * group)
+    other = [j for j in range(Hq) if j // group != head]
+    assert torch.isnan(o[torch.from_numpy(sees)][:, mine]).all()
+    assert same_bits(o, want, ~sees) and torch.equal(ls.cpu()[torch.from_numpy(~sees)], wl.cpu()[torch.from_numpy(~sees)])
+    assert same_bits(o[:, other], want[:, other], np.arange(c.tokens))
+
+
+@pytest.mark.parametrize("splits", (0, 2))
+@pytest.mark.parametrize("i", range(1, len(FORMS)))
+def test_values_past_the_largest_reach_the_rows_that_see_them_alone(i, splits):
+    """Held values of 2^128 and more: as the append writes them (an infinity, and
+    the largest bf16 value, whose code is 2^128), and codes of 2^128 under the
+    largest scales.  A value of 2^119 under the same scale is finite, also
+    beside the weights of up to 2^8 that it is summed with."""
+    lens, news, Hq, H, D, page = FORMS[i]
+    mid = news[0] // 2
+    t, group = lens[0] - news[0] + mid, Hq // H
+    for how in ("inf", "max", 248, 254):
+        say("large values", FORMS[i], splits, how)
+        c = Case(560 + i, lens, news, Hq, H, D, page)
+        q = c.rows(Hq, 2.0)
+        at, slot = c.table[0, t // page], t % page
+        if isinstance(how, str):
+            xv = torch.zeros(c.tokens, H, D, dtype=torch.bfloat16)
+            xv[mid, 0, 5] = float("inf") if how == "inf" else torch.finfo(torch.bfloat16).max
+            run_append(c, xk=c.rows(H), xv=xv)
+            assert c.vs[at, 0] == 247 and ok.decode(c.v[at, 0, 5, slot]) >= 256
+        else:
+            c.v[at, 0], c.vs[at, 0] = 0, how
+            c.v[at, 0, 5, slot] = (262 - how) << 3       # the code of 2^(255 - how)
+        o, ls = attend(c, q, splits=splits)
+        c.v[at, 0, 5, slot] = 0
+        want, wl = attend(c, q, splits=splits)
+        verify(c, q, want, wl)
+        pos = positions(c)
+        sees = (pos[:, 0] == 0) & (pos[:, 1] >= t)
+        assert sees.any() and (~sees).any()
+        assert not torch.isfinite(o[torch.from_numpy(sees)][:, :group, 5]).any()
+        assert same_bits(o, want, ~sees) and torch.equal(ls.cpu()[torch.from_numpy(~sees)], wl.cpu()[torch.from_numpy(~sees)])
+        assert same_bits(o[:, group:], want[:, group:], np.arange(c.tokens))
+        if not isinstance(how, str):
+            c.v[at, 0, 5, slot] = ok.encode(np.float64(2.0 ** (246 - how)))
+            o, ls = attend(c, q, splits=splits)
+            verify(c, q, o, ls)

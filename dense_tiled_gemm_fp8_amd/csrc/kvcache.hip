@@ -44,7 +44,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ float pow2(int32_t e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
+/* 2^e for e in [-149, 127]; under 2^-126 it is subnormal. */
+__device__ __forceinline__ float pow2(int32_t e) { return __builtin_bit_cast(float, e < -126 ? 1u << (e + 149) : (uint32_t)(e + 127) << 23); }
 
 /* New rows of a sequence: rows [row, row + n), the first at position pos
  * (negative where the sequence is shorter than its rows), length len. */
@@ -251,6 +252,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
     if (!begins) e = max(e, e_old);
     const bool grew = !begins && e > e_old;       /* older tokens are rewritten */
     const int32_t ahead = lo - base, upto = hi - base;
+    /* e is up to 128 where the page's scale was byte 255 */
     const float down = pow2(-e), older = pow2(max(e_old - e, -60));
     if (threadIdx.x == 0) *scale = (uint8_t)(e + 127);
 

@@ -659,7 +659,8 @@ typedef struct gemm355_kv_cache {
  *   begins with a new token its scale becomes 2^e; else it becomes the larger
  *   of the old one and 2^e, and if it grew, the codes of the older tokens are
  *   rewritten as the nearest codes of their old values.  Codes are nearest,
- *   ties to even.  The slots behind a sequence's last token stay as they were.
+ *   ties to even; a page of byte 255 keeps it, with codes as under 2^128.  The
+ *   slots behind a sequence's last token stay as they were.
  *   k, v: device bf16, row r head h at k + r * ldk + h * head_dim; finite (an
  *   infinity is held as the largest value, a NaN as a NaN).
  *   q, q_out: the same with q_heads heads, or both NULL; q_out gets bf16 rows

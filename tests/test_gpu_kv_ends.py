@@ -143,3 +143,22 @@ def test_values_past_the_largest_reach_the_rows_that_see_them_alone(i, splits):
             c.v[at, 0, 5, slot] = ok.encode(np.float64(2.0 ** (246 - how)))
             o, ls = attend(c, q, splits=splits)
             verify(c, q, o, ls)
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (256, 128)])
+def test_append_to_pages_of_any_scale(D, page):
+    """Every byte a page's scale can have, kept or grown: new codes are those of
+    its value (a page of byte 255 stays one, its codes as under 2^128)."""
+    for lo in range(0, 256, 64):
+        say("append scales", D, page, lo)
+        c = Case(580 + lo, [page + 5] * 32, [2] * 32, 2, 2, D, page)
+        byte = lo
+        for b in range(32):
+            for h in range(2):
+                c.ks[c.table[b, 1], h], c.vs[c.table[b, 1], h] = byte, 255 - byte
+                byte += 1
+        xk, xv = c.rows(2), c.rows(2)
+        for b in range(32):
+            xk[2 * b] *= 2.0 ** float(c.rng.integers(-100, 126))
+            xv[2 * b:2 * b + 2] *= 2.0 ** float(c.rng.integers(-100, 126))
+        run_append(c, xk=xk, xv=xv)

@@ -727,18 +727,21 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
                 top = row_max(top);
                 /* the reference of a row's weights moves only when its maximum
                  * has passed it by a factor of 2^8: weights stay under 2^8, and
-                 * the sums are rarely touched */
+                 * the sums are rarely touched.  Each row by itself (the others'
+                 * sums are multiplied by 1), so that no row's bits depend on
+                 * another's scores */
                 const float now = fmaxf(m[i], top * p.scale_log2);
+                const bool moves = now > m[i] + 8.0f;
                 float ref = m[i] == -__builtin_inff() ? 0.0f : m[i];       /* no token seen yet */
-                if (__ballot(now > m[i] + 8.0f) != 0) {
-                    ref = now == -__builtin_inff() ? 0.0f : now;
+                if (__ballot(moves) != 0) {
+                    if (moves) ref = now;
                     const float fade = __builtin_amdgcn_exp2f(m[i] - ref);
                     l[i] *= fade;
 #pragma unroll
                     for (int x = 0; x < DT; ++x)
 #pragma unroll
                         for (int y = 0; y < 4; ++y) o[i][x][y] *= fade;
-                    m[i] = now;
+                    if (moves) m[i] = now;
                 }
                 float sum = 0.0f;
 #pragma unroll

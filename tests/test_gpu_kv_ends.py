@@ -162,3 +162,31 @@ def test_append_to_pages_of_any_scale(D, page):
             xk[2 * b] *= 2.0 ** float(c.rng.integers(-100, 126))
             xv[2 * b:2 * b + 2] *= 2.0 ** float(c.rng.integers(-100, 126))
         run_append(c, xk=xk, xv=xv)
+
+
+@pytest.mark.parametrize("splits", (0, 2))
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_rows_of_a_tile_do_not_feel_each_other(i, splits):
+    """A NaN, infinities, and scores far above the others' in some rows: the
+    others keep their bits, whatever the references of those rows do.  So do the
+    rows before a token that changes."""
+    lens, news, Hq, H, D, page = FORMS[i]
+    say("rows alone", FORMS[i], splits)
+    c = Case(600 + i, lens, news, Hq, H, D, page)
+    q = c.rows(Hq)
+    want, wl = attend(c, q, splits=splits)
+    changed = np.zeros((c.tokens, Hq), bool)
+    bad = q.clone()
+    for n, (r, h) in enumerate(((0, 1), (c.tokens - 1, 2), (c.tokens // 2, 0), (c.tokens // 3, 3))):
+        changed[r, h] = True
+        bad[r, h] = float("inf") if n == 1 else 100.0 * bad[r, h]
+        if n == 0:
+            bad[r, h, 5] = float("nan")
+    o, ls = attend(c, bad, splits=splits)
+    assert same_bits(o, want, ~changed) and torch.equal(ls.cpu()[torch.from_numpy(~changed)], wl.cpu()[torch.from_numpy(~changed)])
+    last = lens[0] - 1
+    c.k[c.table[0, last // page], :, last % page] = ok.encode(c.rng.standard_normal((H, D)) * 400)
+    o, ls = attend(c, q, splits=splits)
+    pos = positions(c)
+    sees = (pos[:, 0] == 0) & (pos[:, 1] >= last)
+    assert same_bits(o, want, ~sees) and torch.equal(ls.cpu()[torch.from_numpy(~sees)], wl.cpu()[torch.from_numpy(~sees)])

@@ -48,7 +48,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 __device__ __forceinline__ float pow2(int32_t e) { return __builtin_bit_cast(float, e < -126 ? 1u << (e + 149) : (uint32_t)(e + 127) << 23); }
 
 /* New rows of a sequence: rows [row, row + n), the first at position pos
- * (negative where the sequence is shorter than its rows), length len. */
+ * (negative where the sequence is shorter than its rows), length len.  Rows past
+ * max_new are left out and leave the others where they are. */
 struct Seq {
     int32_t row, n, pos, len;
 };
@@ -56,17 +57,15 @@ struct Seq {
 __device__ __forceinline__ Seq sequence(const KvParams &c, int32_t b)
 {
     Seq s;
+    int32_t rows = c.max_new;
+    s.row = b * c.max_new;
     if (c.q_start) {
-        const int32_t a = min(max(c.q_start[b], 0), c.tokens);
-        const int32_t e = min(max(c.q_start[b + 1], a), c.tokens);
-        s.row = a;
-        s.n = min(e - a, c.max_new);
-    } else {
-        s.row = b * c.max_new;
-        s.n = c.max_new;
+        s.row = min(max(c.q_start[b], 0), c.tokens);
+        rows = min(max(c.q_start[b + 1], s.row), c.tokens) - s.row;
     }
+    s.n = min(rows, c.max_new);
     s.len = min(max(c.lens[b], 0), c.max_len);
-    s.pos = s.len - s.n;
+    s.pos = s.len - rows;
     return s;
 }
 
@@ -212,7 +211,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendParams p, int32_
     const int32_t h = (int32_t)(blockIdx.x >> 1) % c.H, j = (int32_t)(blockIdx.x >> 1) / c.H;
     const int32_t first = max(s.pos, 0);
     const int32_t pg = (first >> c.page_log2) + j, base = pg << c.page_log2;
-    const int32_t lo = max(first, base), hi = min(s.len, base + c.page);
+    const int32_t lo = max(first, base), hi = min(s.pos + s.n, base + c.page);
     if (s.n == 0 || lo >= hi) return;
     const int32_t id = c.table[(int64_t)b * c.table_ld + pg];
     const uint16_t *x = keys ? p.xk + h * D : p.xv + h * D;

@@ -618,7 +618,7 @@ GEMM355_API gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx
  * Device contents that host checks cannot see are bounded by the kernels:
  * lens outside [0, max_len] and q_start outside [0, tokens] or descending are
  * read as the nearest value allowed, rows past max_new in a sequence are left
- * out, and tokens whose page id is not in [0, pages) are neither written nor
+ * out (neither read nor written, the others at their positions), and tokens whose page id is not in [0, pages) are neither written nor
  * seen by any row.  Two sequences may share pages that they only read; a page
  * that a step appends to must belong to one sequence of that step, once.
  */

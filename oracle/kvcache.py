@@ -57,14 +57,16 @@ class Step:
         self.len = [min(max(int(n), 0), max_len) for n in lens]
         self.row: List[int] = []
         self.new: List[int] = []
+        self.pos: List[int] = []          # of a sequence's first row
         for b in range(self.batch):
             if q_start is None:
                 a, n = b * max_new, max_new
             else:
                 a = min(max(int(q_start[b]), 0), tokens)
-                n = min(min(max(int(q_start[b + 1]), a), tokens) - a, max_new)
+                n = min(max(int(q_start[b + 1]), a), tokens) - a
             self.row.append(a)
-            self.new.append(n)
+            self.new.append(min(n, max_new))
+            self.pos.append(self.len[b] - n)
 
     def page_id(self, b: int, t: int) -> Optional[int]:
         i = int(self.table[b, t // self.page])
@@ -76,11 +78,10 @@ def append(step: Step, k: np.ndarray, v: np.ndarray, ks: np.ndarray, vs: np.ndar
     """Updates codes k [pages][H][page][D], v [pages][H][D][page] and scales in
     place; xk, xv: rows x H x D binary64."""
     for b in range(step.batch):
-        n, length = step.new[b], step.len[b]
-        p0 = length - n
+        n, p0 = step.new[b], step.pos[b]
         first = max(p0, 0)
-        for base in range(first // step.page * step.page, length if n else 0, step.page):
-            lo, hi = max(first, base), min(length, base + step.page)
+        for base in range(first // step.page * step.page, p0 + n if n else 0, step.page):
+            lo, hi = max(first, base), min(p0 + n, base + step.page)
             at = step.page_id(b, base)
             if at is None or lo >= hi:
                 continue
@@ -122,7 +123,7 @@ def attention(step: Step, k: np.ndarray, v: np.ndarray, ks: np.ndarray, vs: np.n
         kk = decode(k[pg, :, sl]) * np.ldexp(1.0, ks[pg].astype(int) - 127)[..., None]       # tokens, H, D
         vv = decode(v[pg, :, :, sl]) * np.ldexp(1.0, vs[pg].astype(int) - 127)[..., None]
         for i in range(step.new[b]):
-            p, r = step.len[b] - step.new[b] + i, step.row[b] + i
+            p, r = step.pos[b] + i, step.row[b] + i
             seen = (held <= p) & ((held > p - window) | (held < sinks) if window else True)
             for j in range(Hq):
                 h = j // (Hq // H)

@@ -190,3 +190,28 @@ def test_rows_of_a_tile_do_not_feel_each_other(i, splits):
     pos = positions(c)
     sees = (pos[:, 0] == 0) & (pos[:, 1] >= last)
     assert same_bits(o, want, ~sees) and torch.equal(ls.cpu()[torch.from_numpy(~sees)], wl.cpu()[torch.from_numpy(~sees)])
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32), (256, 128)])
+def test_rows_past_max_new_are_left_out_where_they_are(D, page):
+    """More rows than max_new in a sequence: the first of them keep their
+    positions, the others are neither read nor written."""
+    news = [12, 3, 5]
+    for most in (1, 4, 11):
+        say("rows past max_new", D, page, most)
+        c = Case(620, [90, 40, 7], news, 4, 2, D, page)
+        c.max_new = most
+        out = torch.cat([torch.arange(n) >= most for n in news])
+        q, xk, xv = c.rows(4, 2.0), c.rows(2), c.rows(2, 3.0)
+        for x in (q, xk, xv):
+            x[out] = float("nan")
+        before = [getattr(c, n).copy() for n in ("k", "v")]
+        run_append(c, rot=64, q=False, xk=xk, xv=xv)
+        for b, n in enumerate(news):
+            for t in range(c.lens[b] - n, c.lens[b]):
+                at, slot = c.table[b, t // page], t % page
+                stays = np.array_equal(c.k[at, :, slot], before[0][at, :, slot]) and np.array_equal(c.v[at, :, :, slot], before[1][at, :, :, slot])
+                assert stays == (t >= c.lens[b] - n + most)
+        o, ls = attend(c, q)
+        assert torch.all(o.cpu()[out] == 9.0) and torch.all(ls.cpu()[out] == 9.0) and not torch.any(o.cpu()[~out] == 9.0)
+        verify(c, q, o, ls)

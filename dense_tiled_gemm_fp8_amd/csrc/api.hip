@@ -663,7 +663,8 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     gemm355_status st = check_kv(c, p.c);
     if (st != GEMM355_OK) return st;
     if (a->q_heads < 1 || a->q_heads % c.heads != 0 || a->window < 0 || a->sinks < 0 || a->splits < 0) return GEMM355_EINVAL;
-    if (!(a->scale >= 0.0f) || !(a->scale <= 3.0e38f)) return GEMM355_EINVAL;
+    /* scale * log2(e) stays finite */
+    if (!(a->scale >= 0.0f) || !(a->scale <= 0x1p127f)) return GEMM355_EINVAL;
     p.ldq = a->ldq;
     p.ldo = a->ldo;
     if ((st = check_rows(a->q, p.ldq, c.tokens, a->q_heads, c.head_dim)) != GEMM355_OK) return st;

@@ -711,8 +711,8 @@ GEMM355_API gemm355_status gemm355_kv_append(const gemm355_kv_append_args *args,
  * workspace of its own where scratch is needed (ENOMEM otherwise): a graph's
  * replays would use library-owned memory that later calls may move.
  * Errors: EINVAL (sizes, null pointers, o, lse or the workspace overlapping an
- * input or each other, a scale that is negative or not finite), EALIGN, EUNSUPPORTED, ENOMEM,
- * EHIP.
+ * input or each other, a scale that is negative or above 2^127), EALIGN,
+ * EUNSUPPORTED, ENOMEM, EHIP.
  */
 typedef struct gemm355_attention_args {
     gemm355_kv_cache cache;

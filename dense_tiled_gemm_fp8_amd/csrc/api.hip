@@ -480,15 +480,28 @@ const int64_t kMaxDim = (int64_t)1 << 30;
 const int64_t kMaxWide = (int64_t)1 << 23;
 const int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
 
-/* Extent in bytes of `rows` rows of `cols` elements, ld elements apart. */
+/* Extent in bytes of `rows` rows of `cols` elements, ld elements apart.  Rows of
+ * one pitch that lie beside each other, as columns of one buffer, do not meet. */
 struct Span {
     uintptr_t lo, hi;
-    Span(const void *ptr, uint64_t bytes) : lo((uintptr_t)ptr), hi((uintptr_t)ptr + (ptr ? bytes : 0)) {}
+    uint64_t pitch, width;        /* of several rows; 0: one run of bytes     */
+    Span(const void *ptr, uint64_t bytes) : lo((uintptr_t)ptr), hi((uintptr_t)ptr + (ptr ? bytes : 0)), pitch(0), width(0) {}
     Span(const void *ptr, int64_t rows, int64_t cols, int64_t ld, int64_t es)
         : Span(ptr, rows > 0 && cols > 0 ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * (uint64_t)es : 0)
     {
+        if (rows > 1) {
+            pitch = (uint64_t)(ld * es);
+            width = (uint64_t)(cols * es);
+        }
     }
-    bool meets(const Span &o) const { return lo < o.hi && o.lo < hi && lo < hi && o.lo < o.hi; }
+    bool meets(const Span &o) const
+    {
+        if (!(lo < o.hi && o.lo < hi && lo < hi && o.lo < o.hi)) return false;
+        if (!pitch || pitch != o.pitch) return true;
+        /* where the other's rows begin, counted from the beginnings of these */
+        const uint64_t at = o.lo >= lo ? (o.lo - lo) % pitch : (pitch - (lo - o.lo) % pitch) % pitch;
+        return at < width || at + o.width > pitch;
+    }
 };
 
 bool aligned(const void *ptr, uintptr_t to) { return ((uintptr_t)ptr & (to - 1)) == 0; }

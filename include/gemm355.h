@@ -508,8 +508,10 @@ GEMM355_API gemm355_status gemm355_conv2d_out_size(const gemm355_conv_args *args
  * product.  Weights are held in 4 bits and multiplied by bf16 rows; keys and
  * values are held in 8 bits in pages and read by attention, the other
  * workload that page "The Tensor Core" names as reducing to matrix products.
- * In the arguments below a leading dimension of 0 means packed.  Pointers and
- * the stream belong to the current device.  A graph that a call was captured
+ * In the arguments below a leading dimension of 0 means packed.  Rows of the
+ * same leading dimension in bytes may lie beside each other, as columns of one
+ * buffer, without overlapping.  Pointers and the stream belong to the current
+ * device.  A graph that a call was captured
  * into uses the workspace it was given at every replay: graphs that may run at
  * the same time need different ones, as calls do.
  * ---------------------------------------------------------------------------

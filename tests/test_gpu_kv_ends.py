@@ -215,3 +215,39 @@ def test_rows_past_max_new_are_left_out_where_they_are(D, page):
         o, ls = attend(c, q)
         assert torch.all(o.cpu()[out] == 9.0) and torch.all(ls.cpu()[out] == 9.0) and not torch.any(o.cpu()[~out] == 9.0)
         verify(c, q, o, ls)
+
+
+def test_step_in_columns_of_one_buffer():
+    """A projection's output, the rotated queries, attention's output and the
+    next projection's result side by side in the rows of one buffer."""
+    Hq, H, D, page, T, N = 4, 2, 64, 16, 6, 96
+    c, d = (Case(640, [50, 33], [4, 2], Hq, H, D, page) for _ in range(2))
+    widths = [Hq * D, H * D, H * D, Hq * D, Hq * D, N]
+    at = [int(n) for n in np.cumsum([0] + widths)]
+    arena = torch.full((T, at[-1] + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ld = arena.shape[1]
+    rows = [c.rows(n) for n in (Hq, H, H)]
+    part = [arena[:, a:b] for a, b in zip(at, at[1:])]
+    for n in range(3):
+        part[n].copy_(rows[n].reshape(T, -1))
+    address = [arena.data_ptr() + 2 * n for n in at]
+    codes = torch.randint(0, 256, (N, Hq * D // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((N, Hq * D // 64), 0.125, dtype=torch.bfloat16, device="cuda")
+    m = g.make_w4_matrix(N, Hq * D, codes, scales, group=64)
+    g.gemm355_kv_append(g.make_kv_append_args(c.upload(), address[1], address[2], q=address[0], q_out=address[3], q_heads=Hq,
+                                              ldk=ld, ldv=ld, ldq=ld, ldqo=ld))
+    cache = g.make_kv_cache(c.d["k"], c.d["v"], c.d["ks"], c.d["vs"], pages=c.pages, heads=H, head_dim=D, page=page, table=c.d["table"],
+                            lens=c.d["lens"], batch=2, max_len=c.max_len, q_start=c.d["start"], tokens=T, max_new=4)
+    g.gemm355_attention(g.make_attention_args(cache, address[3], address[4], q_heads=Hq, ldq=ld, ldo=ld))
+    g.gemm355_w4_gemm(T, address[4], m, address[5], ldx=ld, ldy=ld)
+    torch.cuda.synchronize()
+    apart = d.upload()
+    x = [r.cuda() for r in rows]
+    q, o, y = torch.empty_like(x[0]), torch.empty_like(x[0]), torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    g.gemm355_kv_append(g.make_kv_append_args(apart, x[1], x[2], q=x[0], q_out=q, q_heads=Hq))
+    g.gemm355_attention(g.make_attention_args(apart, q, o, q_heads=Hq))
+    g.gemm355_w4_gemm(T, o, m, y)
+    torch.cuda.synchronize()
+    for n, want in zip((0, 1, 2, 3, 4, 5), x + [q, o, y]):
+        assert torch.equal(part[n], want.reshape(T, -1)), n
+    assert torch.isnan(arena[:, at[-1]:]).all() and all(torch.equal(c.d[n], d.d[n]) for n in ("k", "v", "ks", "vs"))

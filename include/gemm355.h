@@ -511,9 +511,9 @@ GEMM355_API gemm355_status gemm355_conv2d_out_size(const gemm355_conv_args *args
  * In the arguments below a leading dimension of 0 means packed.  Rows of the
  * same leading dimension in bytes may lie beside each other, as columns of one
  * buffer, without overlapping.  Pointers and the stream belong to the current
- * device.  A graph that a call was captured
- * into uses the workspace it was given at every replay: graphs that may run at
- * the same time need different ones, as calls do.
+ * device.  A graph that a call was captured into uses the workspace it was given
+ * at every replay: graphs that may run at the same time need different ones, as
+ * calls do.
  * ---------------------------------------------------------------------------
  */
 
@@ -612,17 +612,22 @@ GEMM355_API gemm355_status gemm355_w4_gemm(int64_t M, const void *x, int64_t ldx
  * its token t is slot t % page of page table[b][t / page].  As elsewhere byte
  * 255 of a scale makes its block NaN and a held value of 2^128 or more is an
  * infinity (the append writes one for an infinity and for the largest bf16
- * values, which round up to 2^128).  Its new tokens are
- * rows q_start[b] .. q_start[b + 1] - 1 of the step's tensors and the last of
- * the sequence: row q_start[b] + i has position
- * lens[b] - (q_start[b + 1] - q_start[b]) + i.
+ * values, which round up to 2^128).  The sequence's new tokens are rows
+ * q_start[b] .. q_start[b + 1] - 1 of the step's tensors and its last ones: row
+ * q_start[b] + i has position lens[b] - (q_start[b + 1] - q_start[b]) + i.
  *
  * Device contents that host checks cannot see are bounded by the kernels:
- * lens outside [0, max_len] and q_start outside [0, tokens] or descending are
- * read as the nearest value allowed, rows past max_new in a sequence are left
- * out (neither read nor written, the others at their positions), and tokens whose page id is not in [0, pages) are neither written nor
- * seen by any row.  Two sequences may share pages that they only read; a page
- * that a step appends to must belong to one sequence of that step, once.
+ * lens outside [0, max_len] and q_start outside [0, tokens] are read as the
+ * nearest value allowed, q_start[b + 1] under q_start[b] as q_start[b] (the
+ * outputs of a row that two sequences then name are either's), rows past max_new
+ * in a sequence are left out (neither read nor written, the others at their
+ * positions), and tokens whose page id is not in [0, pages) are neither written
+ * nor seen by any row.  Two sequences may share pages that they only read; a
+ * page that a step appends to must belong to one sequence of that step, once.
+ *
+ * EUNSUPPORTED beside what stands at the members: batch * heads above 65528;
+ * pages above 2^31 - 1; tokens, max_new, max_len, table_ld, a row's width or
+ * leading dimension above 2^30.
  */
 typedef struct gemm355_kv_cache {
     uint8_t *k;             /* E4M3 [pages][heads][page][head_dim]            */
@@ -670,7 +675,9 @@ typedef struct gemm355_kv_cache {
  * All rows 16-byte aligned: pointers (EALIGN), ld* multiples of 8 (EINVAL).
  * One kernel, no scratch.
  * Errors: EINVAL (sizes, null pointers, q_out overlapping an input, the cache
- * overlapping one, rot_len < max_len), EALIGN, EUNSUPPORTED, EHIP.
+ * overlapping one, rot_len < max_len), EALIGN, EUNSUPPORTED (the cache's limits;
+ * a sequence's workgroups, 2 * heads for each page that max_new tokens can touch
+ * and max_new * q_heads * head_dim / 2048, above 2^24 - 1), EHIP.
  */
 typedef struct gemm355_kv_append_args {
     gemm355_kv_cache cache;
@@ -714,7 +721,8 @@ GEMM355_API gemm355_status gemm355_kv_append(const gemm355_kv_append_args *args,
  * replays would use library-owned memory that later calls may move.
  * Errors: EINVAL (sizes, null pointers, o, lse or the workspace overlapping an
  * input or each other, a scale that is negative or above 2^127), EALIGN,
- * EUNSUPPORTED, ENOMEM, EHIP.
+ * EUNSUPPORTED (the cache's limits; max_new * q_heads / heads above 16 * 65535;
+ * more than 2^31 parts in all), ENOMEM, EHIP.
  */
 typedef struct gemm355_attention_args {
     gemm355_kv_cache cache;

@@ -251,3 +251,19 @@ def test_step_in_columns_of_one_buffer():
     for n, want in zip((0, 1, 2, 3, 4, 5), x + [q, o, y]):
         assert torch.equal(part[n], want.reshape(T, -1)), n
     assert torch.isnan(arena[:, at[-1]:]).all() and all(torch.equal(c.d[n], d.d[n]) for n in ("k", "v", "ks", "vs"))
+
+
+@pytest.mark.parametrize("i", range(len(FORMS)))
+def test_attention_scales_from_end_to_end(i):
+    """Scales of 2^-127 to 2^93 for values, to 1 for keys, one size for all or
+    mixed.  (Values of bf16's subnormal range may be lost: they are under 1/50
+    of the largest of their block, and of these few.)"""
+    lens, news, Hq, H, D, page = FORMS[i]
+    say("scales", FORMS[i])
+    c = Case(660 + i, lens, news, Hq, H, D, page)
+    q = c.rows(Hq, 2.0)
+    for low, high in ((0, 0), (1, 1), (8, 8), (60, 60), (220, 220), (90, 105)):
+        c.vs[:] = c.rng.integers(low, high + 1, c.vs.shape)
+        c.ks[:] = c.rng.integers(min(low, 110), min(high, 121) + 1, c.ks.shape)
+        o, ls = attend(c, q)
+        verify(c, q, o, ls)

@@ -528,12 +528,13 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
         for (int x = 0; x < DS; ++x) qf[i][x] = __builtin_bit_cast(bf16x8, *(const u32x4 *)(row + 8 * x));
     }
 
-    f32x4 o[NR][DT];
+    f32x4 o[NR][DT], lw[NR];                      /* lw: sum of the weights as the second product takes them */
     float m[NR], l[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         m[i] = -__builtin_inff();
         l[i] = 0.0f;
+        lw[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int x = 0; x < DT; ++x) o[i][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -589,6 +590,7 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
         for (int x = 0; x < DT; ++x) dma_global16(base + KB + x * 1024, at + 16 * x * c.page);
     };
     constexpr int KEYS = 2 + 4 * DL, VALUES = 1 + DT;   /* copies sent together */
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
 
     int32_t it = begin + wave;
     if (it < end) {
@@ -736,6 +738,7 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
                     if (moves) ref = now;
                     const float fade = __builtin_amdgcn_exp2f(m[i] - ref);
                     l[i] *= fade;
+                    lw[i][0] *= fade;
 #pragma unroll
                     for (int x = 0; x < DT; ++x)
 #pragma unroll
@@ -753,8 +756,7 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
                     }
                 l[i] += sum;
                 /* weights enter the second product in 16 bits: each is off by up
-                 * to 2^-8 of itself, independently, and the output is rounded as
-                 * far */
+                 * to 2^-8 of itself, independently */
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     pf[i][x] = __builtin_bit_cast(bf16x8, u32x4{pack_bf16(s[i][2 * x][0], s[i][2 * x][1]),
@@ -766,6 +768,15 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
             const float vs = __builtin_bit_cast(float, *(const uint32_t *)(own + 2 * KB + 768 + 4 * q) << 23);
             if constexpr (NR == 2 && D <= 128) __builtin_amdgcn_s_setprio(1);
             const u32x4 *vals = (const u32x4 *)(own + KB) + lr * 4 + (q ^ (lr >> 2));
+            /* the sum of the weights as rounded: what divides the other sums,
+             * so that errors they have in common (all, where one token has most
+             * of the weight) go out.  Off 64 bits by 0.0017 of the output's
+             * size for 700 tokens, which is rounding the output, where dividing
+             * by the sum of the unrounded weights is off by 0.0024 */
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < NR; ++i) lw[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf[i][x], lw[i], 0, 0, 0);
 #pragma unroll
             for (int x = 0; x < DT; ++x) {
                 const u32x4 v = vals[x * 64];
@@ -810,7 +821,8 @@ __global__ __launch_bounds__(NW * 64, NR == 2 && D <= 128 ? 2 : 1) void attentio
         const float ref = all[i] == -__builtin_inff() ? 0.0f : all[i];
 #pragma unroll
         for (int w = 0; w < NW; ++w) total[i] += st[w][1][16 * i + lr] * __builtin_amdgcn_exp2f(st[w][0][16 * i + lr] - ref);
-        const float f = __builtin_amdgcn_exp2f(m[i] - ref);
+        /* sums over the rounded weights go on as sums over the others */
+        const float mine = lw[i][0], f = __builtin_amdgcn_exp2f(m[i] - ref) * (mine > 0.0f || mine != mine ? l[i] / mine : 1.0f);
 #pragma unroll
         for (int x = 0; x < DT; ++x) {
             f32x4 v = o[i][x];

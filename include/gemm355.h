@@ -709,8 +709,8 @@ GEMM355_API gemm355_status gemm355_kv_append(const gemm355_kv_append_args *args,
  *   aligned (pointers EALIGN, ld* multiples of 8 EINVAL); o is written.
  *   lse: device fp32 [tokens][q_heads], written, or NULL.
  * Products and statistics are fp32; the softmax weights enter the second
- * product as bf16, and its sums, of values times weights of up to 2^8 before the
- * division by their total, have to stay under 2^128.
+ * product as bf16, whose sums, of values times weights of up to 2^8, are divided
+ * by the sum of the weights as rounded and have to stay under 2^128.
  * The key axis is split into `splits` parts where there are few rows (0:
  * chosen from the sizes; at most one part per 256 tokens); parts go through
  * scratch and a second kernel, in a fixed order, so the same arguments give

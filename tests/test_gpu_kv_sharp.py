@@ -158,3 +158,28 @@ def test_nan_codes_leave_the_rows_that_do_not_see_them(new, splits):
     assert np.array_equal(torch.isnan(o).any(2).cpu().numpy(), heads)
     same = torch.from_numpy(~heads)
     assert torch.equal(o.cpu()[same], want.cpu()[same]) and torch.equal(ls.cpu()[same], wl.cpu()[same])
+
+
+@pytest.mark.parametrize("splits", (0, 3))
+@pytest.mark.parametrize("lens,news,Hq,H,D,page", [([3000, 700], [2, 1], 4, 2, 64, 16), ([3000, 700], [2, 1], 4, 2, 128, 64), ([3000, 700], [2, 1], 8, 2, 256, 32)]
+                         + SHAPES[5:])
+def test_attention_of_equal_values_is_that_value(lens, news, Hq, H, D, page, splits):
+    """Random scores, one value a channel: a mean of it, whatever the weights
+    were rounded to, as the same weights divide it.  Two sums of at most 3000
+    terms, each addition off by 2^-23: under 2^-10, and half a step of bf16 is
+    2^-9 at least."""
+    say("attention equal values", lens, news, Hq, H, D, page, splits)
+    c = Case(760, lens, news, Hq, H, D, page)
+    codes = ok.encode(c.rng.standard_normal((len(lens), H, D)) * 100)
+    value = np.ldexp(ok.decode(codes), -3)
+    c.vs[:] = 124
+    for b, n in enumerate(lens):
+        for t in range(0, n, page):
+            c.v[c.table[b, t // page], :, :, :min(page, n - t)] = codes[b][:, :, None]
+    for scale in (1.0, 4.0):
+        o, ls = attend(c, c.rows(Hq, scale), splits=splits)
+        row = 0
+        for b, n in enumerate(news):
+            want = torch.from_numpy(np.repeat(value[b], Hq // H, 0)).to(torch.bfloat16)
+            assert torch.equal(o[row:row + n].cpu(), want.expand(n, Hq, D)), (scale, b)
+            row += n

@@ -464,11 +464,11 @@ __device__ __forceinline__ void write_out(const AttnParams &p, const Tile &t, in
  *
  * Measured: 64 sequences of 4096 to 8192 tokens, 32 query and 8 key heads of 128,
  * one token: 147 us for 811 MB, 5.5 TB/s: memory.  2 x 65536 tokens, 16 and 2
- * heads: 14.0 us for 59 MB, 4.2 TB/s, as all workgroups begin and end together,
+ * heads: 15.5 us for 59 MB, 3.8 TB/s, as all workgroups begin and end together,
  * and 3.8 us for the join of their parts.  One sequence of 700 tokens, 8 heads of
- * 64: 7.3 us, the chain lengths -> page id -> codes -> two products
+ * 64: 7.5 us, the chain lengths -> page id -> codes -> two products
  * twice over, and the join.  4 x 512 new tokens of 16 and 4 heads of 128 with a
- * window of 2048: 53 us, 0.53 PFLOP/s; of a SIMD's cycles half go to vector
+ * window of 2048: 55 us, 0.51 PFLOP/s; of a SIMD's cycles half go to vector
  * instructions (conversions of codes and exponentials, in equal parts) and a
  * quarter to matrix instructions, and two wavefronts do not hide all of each
  * other's waits.

@@ -206,8 +206,10 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(W4QuantParams p)
 
 /* 8 weights a lane from one dword of codes and their group's scale; exact in fp32
  * (a code less a zero point has 9 bits, a scale 8), rounded once for bf16.  The
- * store bounds it: 8192 x 8192 to bf16, 171 MB in 26 us, 6.6 TB/s with the codes
- * still in the caches; 1000 x 3000 to fp32 4.4 us. */
+ * store bounds it: 8192 x 8192 INT to bf16, 171 MB in 26 us, 6.6 TB/s, right after
+ * the quantiser (codes still in the caches), 37.9 us, 4.5 TB/s, with other
+ * matrices between; to fp32, 305 MB, 61.9 us, 4.9 TB/s.  1000 x 3000 MXFP4 to bf16
+ * 4.0 us, 7.6 MB, to fp32 5.4 us, 13.6 MB: the chain of a load and a store. */
 __global__ __launch_bounds__(256) void w4_dequantize_kernel(W4QuantParams p)
 {
     const Octet o = octet(p);
@@ -383,13 +385,16 @@ __device__ __forceinline__ void store_sums(const W4GemmParams &p, float *store, 
  * across two lines), 32 against 8000 x 7999 17.1, where operands loaded in the
  * matrix order took 192.
  *
- * Measured: one token against 16384 x 8192 INT (groups of 64, zero points), 73 MB
- * in 15.5 us, 4.74 TB/s, what a large copy reaches: memory.  1024 x 1024: 3.0 us,
- * the latency of one round of copies, sums and a join (5 rows against 3000 x 777
- * INT 4.1).  32 tokens against
- * 8192 x 8192 MXFP4: 11.8 us, 3.1 TB/s of codes; every workgroup of 32 rows of W
- * reads all of x, 134 MB from the L2 beside 37 MB from memory, and x takes 8 of a
- * chunk's 10 KB in LDS, so fewer bytes are in flight.
+ * Measured: one token against 16384 x 8192 INT (groups of 64, zero points), 73 MB:
+ * 15.5 us with three matrices in turn, 4.74 TB/s, what a large copy reaches, but
+ * those fit in the 256 MB cache before memory: 19.8 us, 3.7 TB/s, with eleven.
+ * 1024 x 1024: 2.6 us, the latency of one round of copies, sums and a join (5 rows
+ * against 3000 x 777 INT 3.7).  32 tokens against 8192 x 8192 MXFP4: 11.8 us with
+ * three matrices in turn, 15.7 with 18; every workgroup of 32 rows of W reads all
+ * of x, 134 MB from the L2 beside 37 MB of codes, and x takes 8 of a chunk's 10 KB
+ * in LDS, so fewer bytes are in flight.  INT at 32 tokens 19.5, at 64 tokens 31.5
+ * (MXFP4 21.7): there a chunk is 16 KB of x and 2 of codes, of which a wavefront
+ * has room for two.
  */
 template <bool MX, int GROUP, bool ZEROS, int MT, int NT, int NW, bool ODD>
 __global__ __launch_bounds__(NW * 64) void w4_gemm_kernel(W4GemmParams p)
@@ -769,15 +774,20 @@ void launch_one(const W4GemmParams &p, hipStream_t stream)
 }
 
 /* Rows of W a workgroup (16 NT): more of them read x less often, fewer of them
- * make more workgroups, and one a compute unit is wanted (256 of them): 16 rows
- * up to N = 4096, 32 up to 8192, 64 beyond (32 for M <= 4 and M > 32).  us, groups
- * of 64 and 128 INT and MXFP4:
- *   M = 1:  N = 4096, K = 4096   NT 1: 4.2, 2: 4.6;   N = 8000, K = 8064  1: 10.7, 2: 9.6
- *   M = 8:  N = 5120, K = 5120   1: 9.3, 2: 7.4;   N = 8192, K = 8192  2: 12.0, 4: 16.0;
- *           N = 9216, K = 4096   2: 11.0, 4: 9.2
- *   M = 32: N = 4096, K = 4096   1: 6.9, 2: 7.5;   N = 8000  1: 25.0, 2: 18.3;
- *           N = 8192  2: 16.1, 4: 20.5;   N = 9216  2: 17.1, 4: 13.0
- *   M = 64: N = 4096, K = 4096   1: 9.5, 2: 10.4;   N = 8000  1: 40.0, 2: 30.6 */
+ * make more workgroups, and one a compute unit is wanted (the device has 256): 16
+ * rows up to N = 4096, 32 up to 8192, 64 beyond (32 for M <= 4 and M > 32).  us,
+ * INT with groups of 64 and zero points / MXFP4, 14 to 40 matrices in turn:
+ *   M = 1:  N 4096, K 4096   NT 1: 5.1 / 4.2,    2: 5.7 / 4.5
+ *           N 8000, K 8064   NT 1: 13.1 / 9.8,   2: 10.6 / 9.4
+ *   M = 8:  N 5120, K 5120   NT 1: 10.2 / 8.4,   2: 8.1 / 6.5
+ *           N 8192, K 8192   NT 2: 14.4 / 11.4,  4: 20.3 / 15.7
+ *           N 9216, K 4096   NT 2: 12.5 / 9.7,   4: 11.4 / 7.9
+ *   M = 32: N 4096, K 4096   NT 1: 8.7 / 6.7,    2: 10.3 / 7.2
+ *           N 8000, K 8064   NT 1: 27.6 / 24.8,  2: 19.4 / 17.2
+ *           N 8192, K 8192   NT 2: 19.4 / 15.7,  4: 27.6 / 20.4
+ *           N 9216, K 4096   NT 2: 20.0 / 13.4,  4: 16.5 / 11.4
+ *   M = 64: N 4096, K 4096   NT 1: 13.1 / 9.3,   2: 16.4 / 10.0
+ *           N 8000, K 8064   NT 1: 42.3 / 36.8,  2: 31.8 / 24.0 */
 template <bool MX, int GROUP, bool ZEROS>
 void launch_rows(const W4GemmParams &p, hipStream_t stream)
 {

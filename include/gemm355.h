@@ -586,9 +586,9 @@ GEMM355_API gemm355_status gemm355_w4_dequantize(const gemm355_w4_matrix *q, voi
  * gemm355_w4_gemm -- y[m][n] = sum_k x[m][k] W[n][k] for a few bf16 rows x
  * (the skinny end of page "10. Tensor Cores, ...", section "Shape the
  * operation": M of one token or a decode batch, where the stream of weights
- * bounds the time).  Any M >= 0 is right; the work is laid out for M up to 64,
- * beyond that W is read again for every 64 rows and the dense product over
- * dequantised weights is the faster way.
+ * bounds the time).  Any M >= 0 is right; the work is laid out for M up to 64.
+ * Beyond that W is read again for every 64 rows, and the dense product is faster:
+ * from a few hundred rows on also when the weights are dequantised for it alone.
  *   x: device bf16, row m at x + m * ldx, ldx >= K, finite.
  *   y: device, row m at y + m * ldy, ldy >= N, fp32 or bf16 (`out`).
  * Sums are fp32; scales multiply the sum of a group (INT) or the element,

@@ -23,6 +23,7 @@
 #include <unordered_map>
 
 #include "../../include/gemm355.h"
+#include "block.h"
 #include "kernels.h"
 #include "plan.h"
 #include "serve.h"
@@ -668,6 +669,17 @@ gemm355_status append_setup(const gemm355_kv_append_args *a, KvAppendParams &p)
     return GEMM355_OK;
 }
 
+/* Compute units of the current device, 256 without one. */
+int32_t present_cus()
+{
+    int n = 0;
+    if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    return device_cus();
+}
+
 /* Checks, the split of the key axis and the scratch of an attention call. */
 gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, size_t &bytes)
 {
@@ -698,14 +710,7 @@ gemm355_status attention_setup(const gemm355_attention_args *a, AttnParams &p, s
     p.sinks = (int32_t)std::min<int64_t>(a->sinks, c.max_len);
     const int64_t rows = (int64_t)p.c.max_new * p.group;
     if (rows > (int64_t)16 * 65535) return GEMM355_EUNSUPPORTED;
-    const int32_t cus = [] {
-        int n = 0;
-        if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
-            (void)hipGetLastError();
-            return 256;
-        }
-        return device_cus();
-    }();
+    const int32_t cus = present_cus();
     /* Rows a workgroup: 16 while that makes no more workgroups than compute
      * units (heads of 256, whose 32 rows fill the registers: two a unit), else
      * 32, for which a chunk's codes are converted once; us with 16 and 32:
@@ -765,9 +770,291 @@ bool capturing(void *stream)
     return state != hipStreamCaptureStatusNone;
 }
 
+/* ---- block-scaled operators: argument checks ---- */
+
+gemm355_status check_block(const gemm355_block_matrix &q, BlockMat &b)
+{
+    if (q.rows < 0 || q.K < 0 || (q.block_rows != 1 && q.block_rows != 128)) return GEMM355_EINVAL;
+    if (q.rows > ((int64_t)1 << 26) || q.K > kMaxWide) return GEMM355_EUNSUPPORTED;
+    const int64_t nk = (q.K + 127) / 128, least = q.block_rows == 1 ? q.rows : nk;
+    b.ld = q.ld ? q.ld : (q.K + 15) / 16 * 16;
+    b.lds = q.ld_scale ? q.ld_scale : least;
+    if (b.ld < q.K || b.ld % 16 != 0 || b.lds < least) return GEMM355_EINVAL;
+    if (b.ld > kMaxWide || b.lds > kMaxDim) return GEMM355_EUNSUPPORTED;
+    if (q.rows > 0 && q.K > 0 && (!q.codes || !q.scales)) return GEMM355_EINVAL;
+    if (!aligned(q.codes, 16) || !aligned(q.scales, 4)) return GEMM355_EALIGN;
+    b.codes = q.codes;
+    b.scales = q.scales;
+    return GEMM355_OK;
+}
+
+Span block_codes(const gemm355_block_matrix &q, const BlockMat &b) { return Span(b.codes, q.rows, (q.K + 15) / 16 * 16, b.ld, 1); }
+
+Span block_scales(const gemm355_block_matrix &q, const BlockMat &b)
+{
+    const int64_t nk = (q.K + 127) / 128;
+    return q.block_rows == 1 ? Span(b.scales, nk, q.rows, b.lds, 4) : Span(b.scales, (q.rows + 127) / 128, nk, b.lds, 4);
+}
+
+bool block_meets(const gemm355_block_matrix &q, const BlockMat &b, const Span &s)
+{
+    return s.meets(block_codes(q, b)) || s.meets(block_scales(q, b));
+}
+
+bool known(gemm355_src t) { return t == GEMM355_SRC_F32 || t == GEMM355_SRC_BF16; }
+
+/* Rows of one type in device memory: extent, and what may be written in place. */
+struct Rows {
+    const void *ptr;
+    int64_t ld, es;
+    Span span;
+    Rows(const void *p, int64_t rows, int64_t cols, int64_t pitch, gemm355_src type)
+        : ptr(p), ld(pitch ? pitch : cols), es(type == GEMM355_SRC_F32 ? 4 : 2), span(p, rows, cols, ld, es)
+    {
+    }
+    bool same(const Rows &o) const { return ptr == o.ptr && ld == o.ld && es == o.es; }
+    bool vec() const { return aligned(ptr, 16) && ld * es % 16 == 0; }
+};
+
+gemm355_status norm_setup(const gemm355_rmsnorm_args *a, NormParams &p)
+{
+    if (!a || a->rows < 0 || a->width < 0) return GEMM355_EINVAL;
+    if (!known(a->x_type) || !known(a->r_type) || !known(a->w_type) || !known(a->y_type)) return GEMM355_EINVAL;
+    if (!(a->eps > 0.0f) || !(a->eps < INFINITY)) return GEMM355_EINVAL;
+    if (a->rows > ((int64_t)1 << 22) || a->width > ((int64_t)1 << 15)) return GEMM355_EUNSUPPORTED;
+    const int64_t n = a->rows, k = a->width;
+    const Rows x(a->x, n, k, a->ldx, a->x_type), r(a->residual, n, k, a->ldr, a->r_type), h(a->sum, n, k, a->lds, a->r_type),
+        y(a->y, n, k, a->ldy, a->y_type);
+    const Span w(a->weight, (uint64_t)k * (a->w_type == GEMM355_SRC_F32 ? 4 : 2));
+    for (const Rows *t : {&x, &r, &h, &y}) {
+        if (t->ld < k) return GEMM355_EINVAL;
+        if (t->ld > kMaxDim) return GEMM355_EUNSUPPORTED;
+        if (!aligned(t->ptr, (uintptr_t)t->es)) return GEMM355_EALIGN;
+    }
+    if (!aligned(a->weight, a->w_type == GEMM355_SRC_F32 ? 4 : 2)) return GEMM355_EALIGN;
+    p.q = BlockMat{};
+    if (a->q) {
+        if (a->q->rows != n || a->q->K != k || a->q->block_rows != 1) return GEMM355_EINVAL;
+        const gemm355_status st = check_block(*a->q, p.q);
+        if (st != GEMM355_OK) return st;
+    }
+    if (n == 0 || k == 0) return GEMM355_OK;
+    if (!a->x || (a->sum && !a->residual) || (!a->y && !a->q)) return GEMM355_EINVAL;
+    for (const Rows *in : {&x, &r}) {
+        if (h.span.meets(in->span) && !h.same(*in)) return GEMM355_EINVAL;
+        if (y.span.meets(in->span) && !y.same(*in)) return GEMM355_EINVAL;
+    }
+    if (h.span.meets(y.span) || h.span.meets(w) || y.span.meets(w)) return GEMM355_EINVAL;
+    if (a->q) {
+        for (const Span *s : {&x.span, &r.span, &h.span, &y.span, &w})
+            if (block_meets(*a->q, p.q, *s)) return GEMM355_EINVAL;
+        if (block_codes(*a->q, p.q).meets(block_scales(*a->q, p.q))) return GEMM355_EINVAL;
+    }
+    p.x = a->x;
+    p.residual = a->residual;
+    p.weight = a->weight;
+    p.sum = a->sum;
+    p.y = a->y;
+    p.ldx = x.ld;
+    p.ldr = r.ld;
+    p.lds = h.ld;
+    p.ldy = y.ld;
+    p.rows = (int32_t)n;
+    p.width = (int32_t)k;
+    p.x_f32 = x.es == 4;
+    p.r_f32 = r.es == 4;
+    p.w_f32 = a->w_type == GEMM355_SRC_F32;
+    p.y_f32 = y.es == 4;
+    p.vec = x.vec() && (!a->residual || r.vec()) && (!a->sum || h.vec()) && (!a->y || y.vec()) && aligned(a->weight, 16);
+    p.eps = a->eps;
+    return GEMM355_OK;
+}
+
+/* Of the two kinds of products; up and q null for one. */
+struct BlockCall {
+    const gemm355_block_matrix *x, *w, *up, *q;
+    void *y;
+    int64_t ldy;
+    gemm355_src out;
+    int32_t splits;
+    void *workspace;
+    size_t workspace_bytes;
+};
+
+BlockCall block_call(const gemm355_block_gemm_args &a)
+{
+    return BlockCall{&a.x, &a.w, nullptr, nullptr, a.y, a.ldy, a.out, a.splits, a.workspace, a.workspace_bytes};
+}
+
+BlockCall block_call(const gemm355_block_gated_args &a)
+{
+    return BlockCall{&a.x, &a.gate, &a.up, &a.q, a.y, a.ldy, a.out, a.splits, a.workspace, a.workspace_bytes};
+}
+
+/* Checks, plan and scratch of a product.  Of a call with nothing to do p.M or p.N
+ * is 0. */
+gemm355_status block_setup(const BlockCall &c, BlockGemmParams &p, size_t &bytes)
+{
+    BlockMat x, w, up{};
+    gemm355_status st = check_block(*c.x, x);
+    if (st != GEMM355_OK || (st = check_block(*c.w, w)) != GEMM355_OK) return st;
+    if (c.up && (st = check_block(*c.up, up)) != GEMM355_OK) return st;
+    const int64_t M = c.x->rows, N = c.w->rows, K = c.x->K;
+    if (c.x->block_rows != 1 || c.w->block_rows != 128 || c.w->K != K) return GEMM355_EINVAL;
+    if (c.up && (c.up->block_rows != 128 || c.up->K != K || c.up->rows != N)) return GEMM355_EINVAL;
+    if (!known(c.out) || c.splits < 0) return GEMM355_EINVAL;
+    if (M > ((int64_t)1 << 21)) return GEMM355_EUNSUPPORTED;
+    const bool codes = c.q && c.q->codes;
+    p.q = BlockMat{};
+    if (codes) {
+        if (c.q->rows != M || c.q->K != N || c.q->block_rows != 1) return GEMM355_EINVAL;
+        if ((st = check_block(*c.q, p.q)) != GEMM355_OK) return st;
+    }
+    const Rows y(c.y, M, N, c.ldy, c.out);
+    if (y.ld < N) return GEMM355_EINVAL;
+    if (y.ld > kMaxDim) return GEMM355_EUNSUPPORTED;
+    if (!aligned(c.y, (uintptr_t)y.es)) return GEMM355_EALIGN;
+    bytes = 0;
+    p.M = (int32_t)M;
+    p.N = (int32_t)N;
+    if (M == 0 || N == 0) return GEMM355_OK;
+    if (c.up ? codes == (c.y != nullptr) : !c.y) return GEMM355_EINVAL;
+    auto meets = [&](const Span &s) {
+        return block_meets(*c.x, x, s) || block_meets(*c.w, w, s) || (c.up && block_meets(*c.up, up, s));
+    };
+    if (meets(y.span)) return GEMM355_EINVAL;
+    if (codes && (meets(block_codes(*c.q, p.q)) || meets(block_scales(*c.q, p.q)) ||
+                  block_codes(*c.q, p.q).meets(block_scales(*c.q, p.q))))
+        return GEMM355_EINVAL;
+    p.x = x.codes;
+    p.w = w.codes;
+    p.up = up.codes;
+    p.xs = x.scales;
+    p.ws = w.scales;
+    p.us = up.scales;
+    p.ldx = x.ld;
+    p.ldw = w.ld;
+    p.ldu = up.ld;
+    p.lxs = x.lds;
+    p.lws = w.lds;
+    p.lus = up.lds;
+    p.K = (int32_t)K;
+    p.nk = (int32_t)((K + 127) / 128);
+    p.two = c.up != nullptr;
+    p.act = 0;
+    p.y = c.y;
+    p.ldy = y.ld;
+    p.y_f32 = y.es == 4;
+    p.vec = y.vec();
+    const int64_t groups = block_plan(p, c.splits, present_cus());
+    if (groups > kMaxBlocks) return GEMM355_EUNSUPPORTED;
+    const double need = (double)p.part_planes * p.splits * (double)M * (double)p.ldp * 4.0;
+    if (need > 0x1p40) return GEMM355_EUNSUPPORTED;
+    bytes = (size_t)p.part_planes * (size_t)p.splits * (size_t)M * (size_t)p.ldp * sizeof(float);
+    if (bytes && c.workspace) {
+        const Span s(c.workspace, (uint64_t)bytes);
+        if (meets(s) || s.meets(y.span) || (codes && block_meets(*c.q, p.q, s))) return GEMM355_EINVAL;
+    }
+    return GEMM355_OK;
+}
+
+template <class Args>
+gemm355_status block_scratch(const Args *args, size_t *bytes)
+{
+    if (!args || !bytes) return GEMM355_EINVAL;
+    try {
+        BlockGemmParams p;
+        size_t need = 0;
+        const gemm355_status st = block_setup(block_call(*args), p, need);
+        if (st != GEMM355_OK) return st;
+        *bytes = need;
+        return GEMM355_OK;
+    } catch (...) {
+        return GEMM355_ENOMEM;
+    }
+}
+
+gemm355_status block_run(const BlockCall &c, int32_t act, void *stream)
+{
+    try {
+        BlockGemmParams p;
+        size_t need = 0;
+        gemm355_status st = block_setup(c, p, need);
+        if (st != GEMM355_OK || p.M == 0 || p.N == 0) return st;
+        p.act = act;
+        void *ws = nullptr;
+        std::unique_lock<std::mutex> hold;
+        if (need && c.workspace) {
+            if (c.workspace_bytes < need) return GEMM355_ENOMEM;
+            if (!aligned(c.workspace, 256)) return GEMM355_EALIGN;
+            ws = c.workspace;
+        } else if (need) {
+            if (capturing(stream)) return GEMM355_ENOMEM;
+            st = library_scratch(need, stream, &ws, hold);
+            if (st != GEMM355_OK) return st;
+        }
+        p.part = (float *)ws;
+        return launch_block_gemm(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+    } catch (...) {
+        return GEMM355_ENOMEM;   /* the maps of scratch buffers could not grow */
+    }
+}
+
 } /* namespace */
 
 extern "C" {
+
+gemm355_status gemm355_block_quantize(const void *x, int64_t ld, gemm355_src src, const gemm355_block_matrix *q, void *stream)
+{
+    if (!q || !known(src)) return GEMM355_EINVAL;
+    BlockQuantParams p;
+    const gemm355_status st = check_block(*q, p.q);
+    if (st != GEMM355_OK) return st;
+    const Rows rows(x, q->rows, q->K, ld, src);
+    if (rows.ld < q->K) return GEMM355_EINVAL;
+    if (rows.ld > kMaxDim) return GEMM355_EUNSUPPORTED;
+    if (!aligned(x, (uintptr_t)rows.es)) return GEMM355_EALIGN;
+    if (q->rows == 0 || q->K == 0) return GEMM355_OK;
+    if (!x || block_meets(*q, p.q, rows.span) || block_codes(*q, p.q).meets(block_scales(*q, p.q))) return GEMM355_EINVAL;
+    const int64_t per = q->block_rows == 1 ? 16 : 128;
+    if ((q->rows + per - 1) / per * ((q->K + 127) / 128) > kMaxBlocks) return GEMM355_EUNSUPPORTED;
+    p.x = x;
+    p.ldx = rows.ld;
+    p.rows = (int32_t)q->rows;
+    p.K = (int32_t)q->K;
+    p.f32 = rows.es == 4;
+    p.vec = rows.vec();
+    p.block_rows = q->block_rows;
+    return launch_block_quantize(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+}
+
+gemm355_status gemm355_rmsnorm(const gemm355_rmsnorm_args *args, void *stream)
+{
+    NormParams p;
+    const gemm355_status st = norm_setup(args, p);
+    if (st != GEMM355_OK || args->rows == 0 || args->width == 0) return st;
+    return launch_rmsnorm(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
+}
+
+gemm355_status gemm355_block_gemm_workspace(const gemm355_block_gemm_args *args, size_t *bytes) { return block_scratch(args, bytes); }
+
+gemm355_status gemm355_block_gated_workspace(const gemm355_block_gated_args *args, size_t *bytes)
+{
+    if (args && args->act != GEMM355_ACT_SILU && args->act != GEMM355_ACT_GELU_TANH) return GEMM355_EINVAL;
+    return block_scratch(args, bytes);
+}
+
+gemm355_status gemm355_block_gemm(const gemm355_block_gemm_args *args, void *stream)
+{
+    if (!args) return GEMM355_EINVAL;
+    return block_run(block_call(*args), 0, stream);
+}
+
+gemm355_status gemm355_block_gated(const gemm355_block_gated_args *args, void *stream)
+{
+    if (!args || (args->act != GEMM355_ACT_SILU && args->act != GEMM355_ACT_GELU_TANH)) return GEMM355_EINVAL;
+    return block_run(block_call(*args), args->act == GEMM355_ACT_SILU ? 0 : 1, stream);
+}
 
 gemm355_status gemm355_w4_quantize(const void *w, int64_t ld, gemm355_src src, const gemm355_w4_matrix *q, void *stream)
 {

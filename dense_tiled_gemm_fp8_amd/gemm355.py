@@ -43,6 +43,8 @@ FP8_E4M3, FP8_E5M2 = range(2)
 SRC_F32, SRC_BF16 = range(2)
 # formats of a matrix held in 4 bits
 W4_INT, W4_MXFP4 = range(2)
+# activations of the gated pair of products
+ACT_SILU, ACT_GELU_TANH = range(2)
 # layouts
 A_ROW_B_COL, A_ROW_B_ROW, A_COL_B_COL, A_COL_B_ROW = range(4)
 
@@ -134,6 +136,41 @@ class gemm355_attention_args(ctypes.Structure):
     ]
 
 
+class gemm355_block_matrix(ctypes.Structure):
+    _fields_ = [
+        ("rows", _i64), ("K", _i64), ("codes", _vp), ("ld", _i64), ("scales", _vp), ("ld_scale", _i64), ("block_rows", _i32),
+    ]
+
+
+class gemm355_rmsnorm_args(ctypes.Structure):
+    _fields_ = [
+        ("rows", _i64), ("width", _i64),
+        ("x", _vp), ("ldx", _i64), ("x_type", ctypes.c_int),
+        ("residual", _vp), ("ldr", _i64), ("r_type", ctypes.c_int),
+        ("sum", _vp), ("lds", _i64),
+        ("weight", _vp), ("w_type", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("y", _vp), ("ldy", _i64), ("y_type", ctypes.c_int),
+        ("q", ctypes.POINTER(gemm355_block_matrix)),
+    ]
+
+
+class gemm355_block_gemm_args(ctypes.Structure):
+    _fields_ = [
+        ("x", gemm355_block_matrix), ("w", gemm355_block_matrix),
+        ("y", _vp), ("ldy", _i64), ("out", ctypes.c_int), ("splits", _i32),
+        ("workspace", _vp), ("workspace_bytes", _sz),
+    ]
+
+
+class gemm355_block_gated_args(ctypes.Structure):
+    _fields_ = [
+        ("x", gemm355_block_matrix), ("gate", gemm355_block_matrix), ("up", gemm355_block_matrix), ("act", ctypes.c_int),
+        ("y", _vp), ("ldy", _i64), ("out", ctypes.c_int), ("q", gemm355_block_matrix), ("splits", _i32),
+        ("workspace", _vp), ("workspace_bytes", _sz),
+    ]
+
+
 _lib.gemm355_gemm.restype = ctypes.c_int
 _lib.gemm355_gemm.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                               ctypes.c_int, ctypes.c_int, _i32, _i32, _vp]
@@ -181,6 +218,18 @@ _lib.gemm355_attention.restype = ctypes.c_int
 _lib.gemm355_attention.argtypes = [ctypes.POINTER(gemm355_attention_args), _vp]
 _lib.gemm355_attention_workspace.restype = ctypes.c_int
 _lib.gemm355_attention_workspace.argtypes = [ctypes.POINTER(gemm355_attention_args), ctypes.POINTER(_sz)]
+_lib.gemm355_block_quantize.restype = ctypes.c_int
+_lib.gemm355_block_quantize.argtypes = [_vp, _i64, ctypes.c_int, ctypes.POINTER(gemm355_block_matrix), _vp]
+_lib.gemm355_rmsnorm.restype = ctypes.c_int
+_lib.gemm355_rmsnorm.argtypes = [ctypes.POINTER(gemm355_rmsnorm_args), _vp]
+_lib.gemm355_block_gemm.restype = ctypes.c_int
+_lib.gemm355_block_gemm.argtypes = [ctypes.POINTER(gemm355_block_gemm_args), _vp]
+_lib.gemm355_block_gemm_workspace.restype = ctypes.c_int
+_lib.gemm355_block_gemm_workspace.argtypes = [ctypes.POINTER(gemm355_block_gemm_args), ctypes.POINTER(_sz)]
+_lib.gemm355_block_gated.restype = ctypes.c_int
+_lib.gemm355_block_gated.argtypes = [ctypes.POINTER(gemm355_block_gated_args), _vp]
+_lib.gemm355_block_gated_workspace.restype = ctypes.c_int
+_lib.gemm355_block_gated_workspace.argtypes = [ctypes.POINTER(gemm355_block_gated_args), ctypes.POINTER(_sz)]
 _lib.gemm355_status_string.restype = ctypes.c_char_p
 _lib.gemm355_status_string.argtypes = [ctypes.c_int]
 
@@ -190,7 +239,9 @@ EXPORTED = ("gemm355_gemm", "gemm355_gemm_ex", "gemm355_gemm_noalloc",
             "gemm355_tile_info", "gemm355_tile_occupancy", "gemm355_quantize",
             "gemm355_conv2d", "gemm355_conv2d_plan", "gemm355_conv2d_out_size", "gemm355_set_scratch_limit",
             "gemm355_w4_quantize", "gemm355_w4_dequantize", "gemm355_w4_gemm", "gemm355_kv_append",
-            "gemm355_attention", "gemm355_attention_workspace", "gemm355_status_string")
+            "gemm355_attention", "gemm355_attention_workspace", "gemm355_block_quantize", "gemm355_rmsnorm",
+            "gemm355_block_gemm", "gemm355_block_gemm_workspace", "gemm355_block_gated", "gemm355_block_gated_workspace",
+            "gemm355_status_string")
 
 
 class Gemm355Error(RuntimeError):
@@ -423,4 +474,64 @@ def gemm355_attention_workspace(args: gemm355_attention_args) -> int:
     """Scratch bytes of that call (0: none)."""
     n = _sz()
     _check(_lib.gemm355_attention_workspace(ctypes.byref(args), ctypes.byref(n)), "gemm355_attention_workspace")
+    return n.value
+
+
+def make_block_matrix(rows, K, codes=None, scales=None, block_rows=1, ld=0, ld_scale=0) -> gemm355_block_matrix:
+    """Descriptor of a rows x K matrix of E4M3 codes with a scale for each 128
+    K-values of `block_rows` rows; it holds addresses, so the tensors must
+    outlive it."""
+    return gemm355_block_matrix(rows, K, _ptr(codes), ld, _ptr(scales), ld_scale, block_rows)
+
+
+def gemm355_block_quantize(x, matrix: gemm355_block_matrix, src=SRC_BF16, ld=0, stream=None) -> None:
+    """Codes and scales of `matrix` from the rows of x."""
+    _check(_lib.gemm355_block_quantize(_ptr(x), ld, src, ctypes.byref(matrix), _stream(stream)), "gemm355_block_quantize")
+
+
+def make_rmsnorm_args(rows, width, x=None, x_type=SRC_BF16, residual=None, sum=None, r_type=SRC_BF16, weight=None,
+                      w_type=SRC_BF16, eps=1e-5, y=None, y_type=SRC_BF16, q: Optional[gemm355_block_matrix] = None, ldx=0,
+                      ldr=0, lds=0, ldy=0) -> gemm355_rmsnorm_args:
+    return gemm355_rmsnorm_args(rows, width, _ptr(x), ldx, x_type, _ptr(residual), ldr, r_type, _ptr(sum), lds, _ptr(weight),
+                                w_type, eps, _ptr(y), ldy, y_type, ctypes.pointer(q) if q is not None else None)
+
+
+def gemm355_rmsnorm(args: gemm355_rmsnorm_args, stream=None) -> None:
+    """The residual's addition and the norm of its rows, as rows, codes or both."""
+    _check(_lib.gemm355_rmsnorm(ctypes.byref(args), _stream(stream)), "gemm355_rmsnorm")
+
+
+def make_block_gemm_args(x: gemm355_block_matrix, w: gemm355_block_matrix, y=None, out=SRC_BF16, ldy=0, splits=0,
+                         workspace=None, workspace_bytes=0) -> gemm355_block_gemm_args:
+    return gemm355_block_gemm_args(x, w, _ptr(y), ldy, out, splits, _ptr(workspace), workspace_bytes)
+
+
+def gemm355_block_gemm(args: gemm355_block_gemm_args, stream=None) -> None:
+    """y = x times the transpose of w, both with a scale for each block of 128."""
+    _check(_lib.gemm355_block_gemm(ctypes.byref(args), _stream(stream)), "gemm355_block_gemm")
+
+
+def gemm355_block_gemm_workspace(args: gemm355_block_gemm_args) -> int:
+    """Scratch bytes of that call (0: none)."""
+    n = _sz()
+    _check(_lib.gemm355_block_gemm_workspace(ctypes.byref(args), ctypes.byref(n)), "gemm355_block_gemm_workspace")
+    return n.value
+
+
+def make_block_gated_args(x: gemm355_block_matrix, gate: gemm355_block_matrix, up: gemm355_block_matrix, act=ACT_SILU, y=None,
+                          out=SRC_BF16, ldy=0, q: Optional[gemm355_block_matrix] = None, splits=0, workspace=None,
+                          workspace_bytes=0) -> gemm355_block_gated_args:
+    return gemm355_block_gated_args(x, gate, up, act, _ptr(y), ldy, out, q if q is not None else gemm355_block_matrix(), splits,
+                                    _ptr(workspace), workspace_bytes)
+
+
+def gemm355_block_gated(args: gemm355_block_gated_args, stream=None) -> None:
+    """act(x gate^T) * (x up^T), as rows or as codes with scales."""
+    _check(_lib.gemm355_block_gated(ctypes.byref(args), _stream(stream)), "gemm355_block_gated")
+
+
+def gemm355_block_gated_workspace(args: gemm355_block_gated_args) -> int:
+    """Scratch bytes of that call (0: none)."""
+    n = _sz()
+    _check(_lib.gemm355_block_gated_workspace(ctypes.byref(args), ctypes.byref(n)), "gemm355_block_gated_workspace")
     return n.value

@@ -318,9 +318,9 @@ GEMM355_API gemm355_status gemm355_plan(const gemm355_args *args, gemm355_plan_t
  * wave efficiency": split-K's partial sums go to a buffer of their own,
  * combined by a second pass; repacked rows and regrouped block scales use
  * the same buffer).  A call of gemm355_gemm, gemm355_gemm_ex without a
- * workspace, gemm355_conv2d, gemm355_quantize or gemm355_attention that needs more than
- * `bytes` returns ENOMEM before anything is launched, and a buffer is
- * never grown past the cap; buffers already larger are kept until unload.
+ * workspace, gemm355_conv2d, gemm355_quantize, gemm355_attention,
+ * gemm355_block_gemm or gemm355_block_gated that needs more than `bytes` returns
+ * ENOMEM before anything is launched, and a buffer is never grown past the cap; buffers already larger are kept until unload.
  * Calls with a caller workspace and gemm355_gemm_noalloc are not affected.
  * UINT64_MAX (the default) means no cap; 0 refuses every call that needs
  * scratch.  The previous cap goes to *previous (may be NULL).  Process-wide,
@@ -747,6 +747,160 @@ GEMM355_API gemm355_status gemm355_attention(const gemm355_attention_args *args,
  * shape alone can't fix wave efficiency").  Errors: those of
  * gemm355_attention, EINVAL for a NULL bytes. */
 GEMM355_API gemm355_status gemm355_attention_workspace(const gemm355_attention_args *args, size_t *bytes);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Block-scaled operators: matrices of E4M3 codes with an fp32 scale for each
+ * block of 128 K-values (the finer relative of the per-tensor scales of the
+ * E4M3 products; the FP8 pair of page "The Tensor Core", the input/accumulate
+ * table), and what a layer runs on them in turn: the norm that leaves its rows
+ * in this form, the product that reads them, and the gated pair of products that
+ * leaves its own rows in this form for the product behind it.
+ * The conventions are those of the serving operators above.
+ * ---------------------------------------------------------------------------
+ */
+
+/* A rows x K matrix: element k of row r is the value of its code times the scale
+ * of its block.  With blocks of one row (activations) the scale of K block b is
+ * scales[b * ld_scale + r]; with blocks of 128 rows (weights) it is
+ * scales[(r / 128) * ld_scale + b].  The last block of either axis may be short. */
+typedef struct gemm355_block_matrix {
+    int64_t rows, K;        /* any sizes >= 0; EUNSUPPORTED: rows above 2^26, K or
+                               ld above 2^23, ld_scale above 2^30             */
+    uint8_t *codes;         /* device, row r at codes + r * ld, 16-byte aligned
+                               (EALIGN); a row takes K rounded up to 16 bytes, of
+                               which those past K are not written and do not
+                               matter                                         */
+    int64_t ld;             /* a multiple of 16, at least K (EINVAL); 0: K rounded
+                               up to 16                                       */
+    float *scales;          /* device, 4-byte aligned (EALIGN)                */
+    int64_t ld_scale;       /* at least rows, or ceil(K / 128) (EINVAL); 0: that */
+    int32_t block_rows;     /* 1 or 128 (EINVAL otherwise)                    */
+} gemm355_block_matrix;
+
+/* Activations of the gated pair of products. */
+typedef enum gemm355_act {
+    GEMM355_ACT_SILU = 0,       /* g / (1 + exp(-g))                          */
+    GEMM355_ACT_GELU_TANH = 1   /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+} gemm355_act;
+
+/*
+ * gemm355_block_quantize -- rows to codes and scales (section "Practical shape
+ * sweep" of page "10. Tensor Cores, ..." counts quantisation with the product).
+ * For each block, with a = max |x|:
+ *     s = a / 448,  i = 448 / a  in fp32, rounded to nearest (both 1 where a < 2^-100)
+ *     code = the E4M3 code nearest to x * i (rounded to fp32), ties to even
+ *   x: device, row r at x + r * ld, K elements of `src`, finite (what is not gives
+ *   a block of scales and codes without meaning, and nothing worse); ld >= K, 0: K.
+ *   q->codes and q->scales are written.
+ * One kernel, no scratch.  rows or K = 0: nothing is done.
+ * Errors: EINVAL (sizes, enums, null pointers, x, codes and scales overlapping),
+ * EALIGN, EUNSUPPORTED (the matrix's limits; ld above 2^30; more than 2^24 - 1
+ * workgroups, one to 16 rows or 128, whichever have scales of their own, of a K
+ * block), EHIP.
+ */
+GEMM355_API gemm355_status gemm355_block_quantize(const void *x, int64_t ld, gemm355_src src,
+                                      const gemm355_block_matrix *q, void *stream);
+
+/*
+ * gemm355_rmsnorm -- root-mean-square norm of rows with the residual's addition
+ * before it, and rows or codes behind it (what an 8-bit product of section
+ * "Practical shape sweep", page "10. Tensor Cores, ...", is fed from):
+ *     h = x + residual, rounded to the residual's type (h = x without one)
+ *     y = h * w / sqrt(mean(h^2) + eps)
+ * in fp32; sum gets h, y the rows rounded once, q the codes and scales of the
+ * unrounded rows as gemm355_block_quantize gives them (blocks of one row).
+ *   x, residual, sum, y: device rows of `width` elements, ld* elements apart
+ *   (0: width).  residual may be NULL (sum then too), sum may be NULL, weight may be
+ *   NULL (ones).  y or q->codes, or both, are written: not both NULL (EINVAL); q
+ *   may be NULL.  Rows are finite with a sum of squares under 2^128.
+ *   An output may be one of x and residual, in place (same pointer, leading
+ *   dimension and type); any other overlap is EINVAL.
+ * One kernel, no scratch; rows or width = 0: nothing is done.
+ * Errors: EINVAL (sizes, enums, null pointers, overlaps, eps not above 0 or not
+ * finite, q's sizes or its block_rows not 1), EALIGN (pointers to their element),
+ * EUNSUPPORTED (rows above 2^22, width above 2^15, ld* above 2^30), EHIP.
+ */
+typedef struct gemm355_rmsnorm_args {
+    int64_t rows, width;
+    const void *x;        int64_t ldx; gemm355_src x_type;
+    const void *residual; int64_t ldr; gemm355_src r_type;  /* of sum too     */
+    void *sum;            int64_t lds;
+    const void *weight;   gemm355_src w_type;               /* [width]        */
+    float eps;
+    void *y;              int64_t ldy; gemm355_src y_type;
+    const gemm355_block_matrix *q;
+} gemm355_rmsnorm_args;
+
+GEMM355_API gemm355_status gemm355_rmsnorm(const gemm355_rmsnorm_args *args, void *stream);
+
+/*
+ * gemm355_block_gemm -- y[m][n] = sum_b sx[m][b] sw[n / 128][b] sum_{k in b} x[m][k] w[n][k]
+ * for x with blocks of one row and w with blocks of 128 rows (page "10. Tensor
+ * Cores, ...", section "Shape the operation", from one row to many).
+ *   y: device, row m at y + m * ldy, ldy >= w.rows (0: w.rows), fp32 or bf16 (`out`).
+ * A block's inner sum and the sum over blocks are fp32, joined by one fused
+ * multiply-add with the product of the two scales, which is rounded to fp32 and
+ * has to stay under 2^128; codes of x and w are finite.  (A NaN code or scale makes
+ * the outputs that it enters NaN, and no others.)  For rows of bf16 the inner sum
+ * is the 8-bit matrix instruction's: of each 8 products those under 2^-13 of the
+ * largest are cut off, the others to that step.  For rows of fp32 products are
+ * exact and every sum is rounded to 32 bits, at half the rate.
+ * K is split into `splits` parts where there are few tiles (0: chosen from the
+ * sizes; at most 256, and one a K block); parts go through scratch and a second kernel,
+ * in a fixed order, so the same arguments give the same bits.  Scratch is the
+ * caller's workspace (256-byte aligned, EALIGN; at least
+ * gemm355_block_gemm_workspace bytes, ENOMEM) or library-owned (capped by
+ * gemm355_set_scratch_limit); a stream that is being captured needs a workspace of
+ * its own where scratch is needed (ENOMEM otherwise).
+ * x.rows or w.rows = 0: nothing is done; K = 0: y = 0.
+ * Errors: EINVAL (sizes, enums, null pointers, K of x and w not equal, block_rows,
+ * y or the workspace overlapping an input or each other), EALIGN, EUNSUPPORTED (the
+ * matrices' limits; x.rows above 2^21; ldy above 2^30; more than 2^24 - 1
+ * workgroups or 2^40 bytes of scratch), ENOMEM, EHIP.
+ */
+typedef struct gemm355_block_gemm_args {
+    gemm355_block_matrix x, w;
+    void *y;  int64_t ldy; gemm355_src out;
+    int32_t splits;
+    void *workspace;
+    size_t workspace_bytes;
+} gemm355_block_gemm_args;
+
+GEMM355_API gemm355_status gemm355_block_gemm(const gemm355_block_gemm_args *args, void *stream);
+
+/*
+ * gemm355_block_gated -- the gated pair of products of a feed-forward block:
+ *     y = act(x gate^T) * (x up^T)
+ * with each product as gemm355_block_gemm forms it (codes as for bf16), the activation and the product
+ * in fp32 on the unrounded sums.  gate and up have the same sizes.  Either rows y
+ * are written (as there), or q: codes and scales of the unrounded rows as
+ * gemm355_block_quantize gives them (blocks of one row), ready to be the x of the
+ * product behind it.  Of y and q.codes exactly one is not NULL (EINVAL).
+ * splits, scratch, sizes of zero and errors as for gemm355_block_gemm, the outputs
+ * being y, or q's codes and scales.  Codes out for a few rows go through scratch
+ * also where K is not split: a scale needs 128 columns.
+ */
+typedef struct gemm355_block_gated_args {
+    gemm355_block_matrix x, gate, up;
+    gemm355_act act;
+    void *y;  int64_t ldy; gemm355_src out;
+    gemm355_block_matrix q;
+    int32_t splits;
+    void *workspace;
+    size_t workspace_bytes;
+} gemm355_block_gated_args;
+
+GEMM355_API gemm355_status gemm355_block_gated(const gemm355_block_gated_args *args, void *stream);
+
+/* Scratch of those calls in bytes (0: none), to *bytes, a host pointer.  Host
+ * arithmetic over the sizes and the current device's compute units (256 without a
+ * device); pointers are checked as by the calls, never read.  The partial sums are
+ * the counterpart of split-K's (page "10. Tensor Cores, ...", section "When shape
+ * alone can't fix wave efficiency").  Errors: those of the calls, EINVAL for a NULL
+ * bytes. */
+GEMM355_API gemm355_status gemm355_block_gemm_workspace(const gemm355_block_gemm_args *args, size_t *bytes);
+GEMM355_API gemm355_status gemm355_block_gated_workspace(const gemm355_block_gated_args *args, size_t *bytes);
 
 /* Static description of a status code (this library's own codes; no
  * passage of the pages defines them).  Never NULL: unknown codes get a

@@ -57,6 +57,7 @@ struct BlockGemmParams {
     /* the plan (block_plan) */
     int32_t exact;                /* 1: products in bf16, summed in fp32     */
     int32_t form;                 /* kernel: index of its table              */
+    int32_t resident;             /* workgroups that run at once             */
     int32_t splits;               /* parts of K; more than one, or rows that
                                      wait for their scale, go through `part` */
     int32_t part_planes;          /* 0: none; fp32 planes [M][ldp] a part    */

@@ -20,6 +20,7 @@
  * instruction sums them in fp32 at half the rate.
  *
  *   block_rows_kernel    few tokens: the stream of weights counts
+ *   block_tile_kernel    many tokens: the matrix units count
  *   block_finish_kernel  joins parts of K, activates, quantises
  */
 #include <hip/hip_runtime.h>
@@ -39,6 +40,7 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -276,6 +278,466 @@ __global__ __launch_bounds__(NW * 64) void block_rows_kernel(BlockGemmParams p)
     }
 }
 
+/* Values of a lane of a 32 x 32 matrix block (token lane % 32; columns 8 q + 4 h .. + 3
+ * for q < 4, h = lane / 32) to memory, lanes h = 0 and 1 beside each other. */
+struct Place {
+    int32_t m, n;                 /* the lane's token, the block's first column */
+    int h;
+};
+
+/* Swaps the upper 32 lanes of a with the lower 32 of b. */
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+__device__ __forceinline__ void store_part(const BlockGemmParams &p, float *plane, const Place &at, const f32x16 &v)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int32_t n = at.n + 8 * q + 4 * at.h;
+        f32x4 t;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = v[4 * q + e];
+        if (at.m < p.M && n < p.N) *(f32x4 *)(plane + (int64_t)at.m * p.ldp + n) = t;
+    }
+}
+
+__device__ __forceinline__ void store_rows(const BlockGemmParams &p, const Place &at, const f32x16 &v)
+{
+    if (p.vec && !p.y_f32) {
+        /* 8 columns a lane: quads 0 and 1 (2 and 3) of both halves trade places */
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+            uint32_t d[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float a = v[4 * (q + j) + 2 * i], b = v[4 * (q + j) + 2 * i + 1];
+                    d[j][i] = pack_bf16(a, b);
+                }
+            swap32(d[0][0], d[1][0]);
+            swap32(d[0][1], d[1][1]);
+            const int32_t n = at.n + 8 * (q + at.h);
+            if (at.m >= p.M || n >= p.N) continue;
+            uint16_t *o = (uint16_t *)p.y + (int64_t)at.m * p.ldy + n;
+            if (n + 8 <= p.N) {
+                *(uint4 *)o = make_uint4(d[0][0], d[0][1], d[1][0], d[1][1]);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (n + j < p.N) o[j] = (uint16_t)(d[j >> 2][(j >> 1) & 1] >> (16 * (j & 1)));
+        }
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        f32x4 t;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = v[4 * q + e];
+        if (at.m < p.M) store4(p, at.m, at.n + 8 * q + 4 * at.h, t);
+    }
+}
+
+__device__ __forceinline__ void store_codes(const BlockGemmParams &p, const Place &at, const f32x16 &v, float inverse)
+{
+    uint32_t d[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = v[4 * q + e] * inverse;
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+        d[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], w, true);
+    }
+    /* 16 columns a lane: dwords of quads 0, 1 for h = 0, of 2, 3 for h = 1 */
+    swap32(d[0], d[2]);
+    swap32(d[1], d[3]);
+    const int32_t n = at.n + 16 * at.h;
+    if (at.m >= p.M || n >= p.N) return;
+    uint8_t *o = p.q.codes + (int64_t)at.m * p.q.ld + n;
+    if (n + 16 <= p.N) {
+        *(uint4 *)o = make_uint4(d[0], d[2], d[1], d[3]);
+        return;
+    }
+    const uint32_t w[4] = {d[0], d[2], d[1], d[3]};
+#pragma unroll
+    for (int j = 0; j < 15; ++j)
+        if (n + j < p.N) o[j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+}
+
+/*
+ * TX tokens and TW rows of w (of two matrices: TW / 2 of each, of the same columns)
+ * a tile, a workgroup of WX x WW wavefronts, one K block of 128 a stage of a ring of
+ * two.  A wavefront's block is two by FW matrix blocks of 32 x 32, in a row of two
+ * at a time: the sums of a K block come from two instructions each, begun at zero,
+ * and the multiply-adds of them into the fp32 sums run while the matrix unit has the
+ * instruction behind: the first's during the second's, the second's during the next
+ * row's first.  Fragments are read into their own registers again right after their
+ * last use.
+ *
+ * A stage is rows of 128 bytes (a row's 16-byte unit c lies at c ^ (row / 2 % 8)),
+ * the tokens' scales and the weights'.  Before the last row of matrix blocks of a K
+ * block is a barrier: by then every fragment of the stage has been read and the
+ * next stage has landed, and the weights' copies of the K block two ahead follow it.
+ * The tokens' fragments have been read by all one row earlier (FW > 2: a second
+ * barrier, before row 1), and the tokens' copies go there, so that the copies of a
+ * K block come in two bursts.
+ *
+ * A workgroup takes every gridDim.x-th unit (a tile's part of K).  The first copies
+ * of its next unit land before it stores the sums of this one, from registers, and
+ * nothing waits for the stores before the unit's second K block.
+ */
+template <int TX, int TW, int WX, int WW, int MINB, bool TWO, bool EXACT>
+__global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemmParams p)
+{
+    constexpr int NW = WX * WW, WTX = TX / WX, WTW = TW / WW, FX = WTX / 32, FW = WTW / 32;
+    constexpr int XB = TX * 128, WB = TW * 128, SCX = XB + WB, SCW = SCX + TX * 4, STAGE = SCW + 256;
+    constexpr int XL = TX / 8 / NW, WL = TW / 8 / NW, LOADS = XL + WL + 1;
+    constexpr int OC = TWO ? WTW / 2 : WTW, OF = OC / 32, TN = TWO ? TW / 2 : TW;   /* columns out */
+    constexpr int SCG = TX / 64 + 1;               /* scale copies of a stage */
+    constexpr bool EARLY = FW > 2;                 /* tokens' copies in row 1 */
+    static_assert(FX == 2 && NW >= SCG && NW % 2 == 0 && WTW <= 128 && LOADS < 64, "tile");
+    static_assert(!TWO || (NW * 8 == WTW / 2), "a copy is of one matrix");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE + WW * TX * 4];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wx = wave / WW, ww = wave % WW;
+    const int32_t tm = (p.M + TX - 1) / TX, tn = (p.N + TN - 1) / TN, units = tm * tn * p.splits;
+    const uint32_t base = lds_addr(smem);
+    /* the scale copies of a stage go round the wavefronts (those past the last
+     * repeat the first: the same values to the same place) */
+    const int sg = wave % SCG;
+    const int64_t sc_step = sg < SCG - 1 ? p.lxs : 1;
+
+    /* the unit in hand, and what its copies need of a lane */
+    int32_t m0, n0, part, k0, k1, have;
+    i32x4 rx, rw, ru;
+    uint32_t xoff[XL], woff[WL];
+    const float *sc;
+    int lane, unit;
+    auto setup = [&](int32_t id) __attribute__((always_inline)) {
+        /* formed from a lane index that the compiler cannot see through, or it
+         * would hold all of this across units */
+        lane = lane_id();
+        asm volatile("" : "+v"(lane));
+        part = id / (tm * tn);
+        const int32_t t = id - part * (tm * tn);
+        /* neighbouring units share operands: bands of 4 rows of tiles */
+        const int32_t band = t / (4 * tn), in = t - band * 4 * tn, high = std::min(4, tm - band * 4);
+        m0 = (band * 4 + in % high) * TX;
+        n0 = in / high * TN;
+        k0 = kslice_begin(p.nk, p.splits, part);
+        k1 = kslice_begin(p.nk, p.splits, part + 1);
+        /* copy d of 8 rows: the lane's row, and the unit that belongs at its place
+         * (rows of d and d + 1 are NW * 8 apart: a multiple of 16) */
+        const int drow = lane >> 3;
+        unit = (lane & 7) ^ ((4 * wave + (drow >> 1)) & 7);
+        rx = rsrc_words(p.x + (int64_t)m0 * p.ldx);
+        rw = rsrc_words(p.w + (int64_t)n0 * p.ldw);
+        if constexpr (TWO) ru = rsrc_words(p.up + (int64_t)n0 * p.ldu);
+#pragma unroll
+        for (int d = 0; d < XL; ++d) {
+            const int r = (d * NW + wave) * 8 + drow;
+            xoff[d] = m0 + r < p.M ? (uint32_t)(r * (int32_t)p.ldx + unit * 16) : kOOB;
+        }
+#pragma unroll
+        for (int d = 0; d < WL; ++d) {
+            int r = (d * NW + wave) * 8 + drow;
+            if constexpr (TWO) r = r / WTW * OC + r % OC;
+            woff[d] = n0 + r < p.N ? (uint32_t)(r * (int32_t)(TWO && (d & 1) ? p.ldu : p.ldw) + unit * 16) : kOOB;
+        }
+        /* rows past the last repeat its scale */
+        if (sg < SCG - 1)
+            sc = p.xs + std::min(m0 + sg * 64 + lane, p.M - 1);
+        else if (TWO)
+            sc = lane & 1 ? p.us + (int64_t)(n0 >> 7) * p.lus : p.ws + (int64_t)(n0 >> 7) * p.lws;
+        else
+            sc = p.ws + (int64_t)(std::min(n0 + (lane & 1) * 128, p.N - 1) >> 7) * p.lws;
+        sc += k0 * sc_step;
+        /* K blocks whose unit of this lane lies before K, in this part */
+        have = std::min(k1, (p.K - unit * 16 + 127) >> 7);
+    };
+    auto copy = [&](auto dc, int32_t kb, uint32_t so) __attribute__((always_inline)) {
+        constexpr int d = decltype(dc)::value;
+        /* kOOB and an offset along a row stay out of range */
+        const uint32_t k = (uint32_t)kb * 128;
+        if constexpr (d < XL) {
+            dma16<d * NW * 1024>(rx, base + so + wave * 1024, kb < have ? xoff[d] + k : kOOB);
+        } else if constexpr (d < XL + WL) {
+            dma16<XB + (d - XL) * NW * 1024>(TWO && ((d - XL) & 1) ? ru : rw, base + so + wave * 1024,
+                                             kb < have ? woff[d - XL] + k : kOOB);
+        } else {
+            dma_global4(base + so + SCX + sg * 256, sc);
+            if (kb + 1 < k1) sc += sc_step;
+        }
+    };
+    auto first_copies = [&]() __attribute__((always_inline)) {
+        if (k1 <= k0) return;
+        unroll<LOADS>([&](auto dc) __attribute__((always_inline)) { copy(dc, k0, 0u); });
+        unroll<LOADS>([&](auto dc) __attribute__((always_inline)) { copy(dc, k0 + 1, (uint32_t)STAGE); });
+    };
+    /* K ends inside a unit: the lanes that copied it clear what lies behind, once it
+     * has landed */
+    auto clear_tail = [&](int32_t kb, uint32_t so) __attribute__((always_inline)) {
+        if ((p.K & 15) == 0 || kb != p.nk - 1 || kb >= k1) return;
+        const int32_t left = p.K - kb * 128 - unit * 16;
+        if (left > 0 && left < 16) {
+            const uint64_t lo = left >= 8 ? ~0ull : (1ull << (8 * left)) - 1, hi = left <= 8 ? 0 : (1ull << (8 * (left - 8))) - 1;
+            uint64_t *u = (uint64_t *)(smem + so + wave * 1024 + lane * 16);
+#pragma unroll 1
+            for (int d = 0; d < XL + WL; ++d, u += NW * 128) {
+                u[0] &= lo;
+                u[1] &= hi;
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+
+    const int32_t round = xcd_remap(blockIdx.x, gridDim.x);
+    int32_t id = round;
+    if (id >= units) return;
+    setup(id);
+    first_copies();
+    if (k1 > k0) wait_vmcnt<LOADS>();
+    bool both = false;            /* the first two K blocks have landed */
+    for (;;) {
+        f32x16 acc[FW][2];
+#pragma unroll
+        for (int f = 0; f < FW; ++f)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) acc[f][x] = f32x16{};
+
+        if (k1 > k0) {
+            const int frow = lane & 31, h = lane >> 5, sw = (frow >> 1) & 7;
+            auto frag = [&](uint32_t rows, int s) __attribute__((always_inline)) {
+                const uint8_t *row = smem + rows + frow * 128;
+                const i32x4 lo = *(const i32x4 *)(row + (((4 * s + 2 * h) ^ sw) << 4));
+                const i32x4 hi = *(const i32x4 *)(row + (((4 * s + 2 * h + 1) ^ sw) << 4));
+                return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            };
+            i32x8 xf[2][2], wf[2];
+            float sx[2], sw_[2];
+            auto read_w = [&](uint32_t so, int f, int s) __attribute__((always_inline)) {
+                wf[s] = frag(so + XB + (ww * WTW + f * 32) * 128, s);
+            };
+            auto read_x = [&](uint32_t so, int x, int s) __attribute__((always_inline)) {
+                xf[x][s] = frag(so + (wx * WTX + x * 32) * 128, s);
+            };
+            auto read_scales = [&](uint32_t so) __attribute__((always_inline)) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) sx[x] = *(const float *)(smem + so + SCX + (wx * WTX + x * 32 + frow) * 4);
+                sw_[0] = *(const float *)(smem + so + SCW + (TWO ? 0 : ww * WTW / 128 * 4));
+                sw_[1] = TWO ? *(const float *)(smem + so + SCW + 4) : 0.0f;
+            };
+
+            /* the unit's first K block has landed */
+            clear_tail(k0, 0);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                read_x(0, 0, s);
+                read_x(0, 1, s);
+                read_w(0, 0, s);
+            }
+            read_scales(0);
+
+            f32x16 sum[2];
+            float scale[2][2], last = 0.0f;
+            sum[0] = sum[1] = f32x16{};
+            uint32_t so = 0;
+            auto multiply = [&](int x, int s) __attribute__((always_inline)) {
+                f32x16 v = s ? sum[x] : f32x16{};
+                if constexpr (EXACT) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(wf[s], i), widen(xf[x][s], i), v, 0, 0, 0);
+                } else {
+                    v = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[s], xf[x][s], v, 0, 0, 0, 0, 0, 0);
+                }
+                sum[x] = v;
+            };
+            auto add = [&](f32x16 &a, int x, float by) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) a[e] = __builtin_fmaf(sum[x][e], by, a[e]);
+                /* here, not where the sums are next used */
+                asm volatile("" : "+v"(a));
+            };
+            auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
+            for (int32_t kb = k0; kb < k1; ++kb) {
+                const uint32_t next = so ^ (uint32_t)STAGE;
+                unroll<FW>([&](auto fc) __attribute__((always_inline)) {
+                    constexpr int f = decltype(fc)::value;
+                    constexpr bool end = f == FW - 1;
+                    constexpr int m = TWO && f >= FW / 2 ? 1 : 0;
+                    /* this row's copies: a quarter behind each instruction */
+                    constexpr int c0 = EARLY && end ? XL : 0, c1 = EARLY ? f == 1 ? XL : end ? LOADS : 0 : end ? LOADS : 0;
+                    auto copies = [&](auto qc) __attribute__((always_inline)) {
+                        constexpr int q = decltype(qc)::value;
+                        unroll<LOADS>([&](auto dc) __attribute__((always_inline)) {
+                            constexpr int d = decltype(dc)::value;
+                            if constexpr (d >= c0 && d < c1 && (d - c0) * 4 / (c1 - c0) == q) copy(dc, kb + 2, so);
+                        });
+                    };
+                    if constexpr (EARLY && f == 1) {
+                        __builtin_amdgcn_s_barrier();
+                        asm volatile("" ::: "memory");
+                    }
+                    if constexpr (end) {
+                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                        /* (of a workgroup's later units the first two have landed
+                         * before: stores of the unit before are not waited for yet) */
+                        if (!both) wait_vmcnt<EARLY ? XL : 0>();
+                        both = false;
+                        clear_tail(kb + 1, next);
+                        __builtin_amdgcn_s_barrier();
+                        asm volatile("" ::: "memory");
+                    }
+                    multiply(0, 0);
+                    fence();
+                    if constexpr (end) read_x(next, 0, 0);
+                    copies(std::integral_constant<int, 0>{});
+                    /* the row before: of the K block before for the first */
+                    add(acc[f == 0 ? FW - 1 : f - 1][1], 1, f == 0 ? last : scale[TWO && f - 1 >= FW / 2 ? 1 : 0][1]);
+                    fence();
+                    multiply(1, 0);
+                    fence();
+                    if constexpr (f == 0) {
+                        /* not before: their reads were the last ones */
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            scale[0][x] = sx[x] * sw_[0];
+                            if (TWO) scale[1][x] = sx[x] * sw_[1];
+                        }
+                    }
+                    read_w(end ? next : so, end ? 0 : f + 1, 0);
+                    if constexpr (end) read_x(next, 1, 0);
+                    copies(std::integral_constant<int, 1>{});
+                    fence();
+                    multiply(0, 1);
+                    fence();
+                    if constexpr (end) read_x(next, 0, 1);
+                    copies(std::integral_constant<int, 2>{});
+                    fence();
+                    multiply(1, 1);
+                    fence();
+                    read_w(end ? next : so, end ? 0 : f + 1, 1);
+                    if constexpr (end) {
+                        read_x(next, 1, 1);
+                        read_scales(next);
+                    }
+                    copies(std::integral_constant<int, 3>{});
+                    add(acc[f][0], 0, scale[m][0]);
+                    fence();
+                });
+                last = scale[TWO ? 1 : 0][1];
+                so = next;
+            }
+            add(acc[FW - 1][1], 1, last);
+        }
+
+        /* every fragment has been read and the copies of K blocks past the last have
+         * landed: the ring is free for the next unit */
+        wait_vmcnt<0>();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        const int32_t mw = m0 + wx * WTX, nw = n0 + ww * OC, nb = n0 >> 7, from = part;
+        id += gridDim.x;
+        const bool more = id < units;
+        if (more) {
+            setup(id);
+            first_copies();
+        }
+
+        int el = lane_id();
+        asm volatile("" : "+v"(el));
+        const int h = el >> 5;
+        const bool activate = TWO && (p.part_planes < 2);
+        if constexpr (TWO) {
+            if (activate) {
+#pragma unroll
+                for (int f = 0; f < OF; ++f)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float a = acc[f][x][e], b = acc[OF + f][x][e];
+                            acc[f][x][e] = gated(a, b, p.act);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            }
+        }
+        if (more) {
+            wait_vmcnt<0>();
+            both = true;
+        }
+        if (p.part_planes) {
+            const int64_t plane = (int64_t)p.M * p.ldp;
+            float *o = p.part + (int64_t)from * p.part_planes * plane;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int f = 0; f < OF; ++f) {
+                    const Place at{mw + x * 32 + (el & 31), nw + f * 32, h};
+                    store_part(p, o, at, acc[f][x]);
+                    if constexpr (TWO)
+                        if (!activate) store_part(p, o + plane, at, acc[OF + f][x]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        } else if (TWO && p.q.codes) {
+            /* a row's 128 columns are those of the WW wavefronts beside each other */
+            float *red = (float *)(smem + 2 * STAGE);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float a = 0.0f;
+#pragma unroll
+                for (int f = 0; f < OF; ++f)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float v = acc[f][x][e];
+                        a = fmaxf(a, fabsf(v));
+                    }
+                a = fmaxf(a, __shfl_xor(a, 32, 64));
+                red[ww * TX + wx * WTX + x * 32 + (el & 31)] = a;
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float a = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WW; ++w) a = fmaxf(a, red[w * TX + wx * WTX + x * 32 + (el & 31)]);
+                const bool none = a < 0x1p-100f;
+                const float inverse = none ? 1.0f : 448.0f / a;
+                const int32_t m = mw + x * 32 + (el & 31);
+                if (ww == 0 && h == 0 && m < p.M) p.q.scales[(int64_t)nb * p.q.lds + m] = none ? 1.0f : a / 448.0f;
+#pragma unroll
+                for (int f = 0; f < OF; ++f) {
+                    store_codes(p, Place{m, nw + f * 32, h}, acc[f][x], inverse);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int f = 0; f < OF; ++f) {
+                    store_rows(p, Place{mw + x * 32 + (el & 31), nw + f * 32, h}, acc[f][x]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        }
+        if (!more) break;
+    }
+}
+
 /* One row's 128 columns to 16 lanes: the sum over the parts in ascending order (of
  * both planes where there are two), the activation, and rows or codes. */
 __global__ __launch_bounds__(256) void block_finish_kernel(BlockGemmParams p)
@@ -292,8 +754,11 @@ __global__ __launch_bounds__(256) void block_finish_kernel(BlockGemmParams p)
             for (int j = 0; j < 2; ++j) {
                 /* ldp is a multiple of 4, and at least N */
                 if (n + 4 * j >= p.N) continue;
-                v[j] += *(const f32x4 *)(o + 4 * j);
-                if (p.part_planes == 2) u[j] += *(const f32x4 *)(o + plane + 4 * j);
+                const f32x4 a = *(const f32x4 *)(o + 4 * j);
+                v[j] = s ? v[j] + a : a;       /* a zero keeps its sign */
+                if (p.part_planes < 2) continue;
+                const f32x4 b = *(const f32x4 *)(o + plane + 4 * j);
+                u[j] = s ? u[j] + b : b;
             }
     }
     float e[8], a = 0.0f;
@@ -332,15 +797,23 @@ __global__ __launch_bounds__(256) void block_finish_kernel(BlockGemmParams p)
 
 int64_t block_plan(BlockGemmParams &p, int32_t splits, int32_t cus)
 {
-    (void)cus;
-    p.form = p.M <= 16 ? 0 : 1;
+    p.exact = p.y && p.y_f32;
+    const int32_t force = splits >> 16;     /* TIMING */
+    splits &= 0xFFFF;
+    p.form = force ? force - 1 : p.M <= 16 ? 0 : p.M <= 64 ? 1 : 2;
+    if (p.form == 3 && p.exact) p.form = 2;
+    int64_t units = 1;
+    if (p.form >= 2) {
+        const int32_t tx = p.form == 2 ? 128 : 256, tn = (p.form == 2 ? 128 : 256) >> p.two;
+        units = ((int64_t)p.M + tx - 1) / tx * (((int64_t)p.N + tn - 1) / tn);
+    }
+    p.resident = p.form == 2 ? 2 * cus : cus;
     p.splits = std::max(1, std::min({splits, p.nk, 256}));
-    /* a workgroup has 16 columns of two matrices, and a scale needs 128 */
-    p.part_planes = p.splits > 1 ? 1 + p.two : p.q.codes ? 1 : 0;
+    /* a scale of codes needs 128 columns in one workgroup */
+    p.part_planes = p.splits > 1 ? 1 + p.two : p.q.codes && p.form != 3 ? 1 : 0;
     p.ldp = ((int64_t)p.N + 3) / 4 * 4;
     p.part = nullptr;
-    p.exact = p.y && p.y_f32;
-    return (((int64_t)p.M + 15) / 16) * (((int64_t)p.N + 127) / 128);
+    return std::max(units * p.splits, (((int64_t)p.M + 15) / 16) * (((int64_t)p.N + 127) / 128));
 }
 
 namespace {
@@ -360,14 +833,32 @@ void launch_rows(const BlockGemmParams &p, hipStream_t stream)
         hipLaunchKernelGGL((block_rows_kernel<FX, 2, NW, ST, false, false>), grid, block, 0, stream, p);
 }
 
+template <int TX, int TW, int WX, int WW, int MINB, bool EXACT>
+void launch_tile(const BlockGemmParams &p, int64_t most, hipStream_t stream)
+{
+    const int64_t tn = p.two ? TW / 2 : TW;
+    const int64_t units = (((int64_t)p.M + TX - 1) / TX) * ((p.N + tn - 1) / tn) * p.splits;
+    const dim3 grid((uint32_t)std::min(units, most)), block(WX * WW * 64);
+    if (p.two)
+        hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, MINB, true, EXACT>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, MINB, false, EXACT>), grid, block, 0, stream, p);
+}
+
 } /* namespace */
 
 hipError_t launch_block_gemm(const BlockGemmParams &p, hipStream_t stream)
 {
     if (p.form == 0)
         launch_rows<1, 8, 3>(p, stream);
-    else
+    else if (p.form == 1)
         launch_rows<4, 4, 3>(p, stream);
+    else if (p.form == 2 && p.exact)
+        launch_tile<128, 128, 2, 2, 2, true>(p, p.resident, stream);
+    else if (p.form == 2)
+        launch_tile<128, 128, 2, 2, 2, false>(p, p.resident, stream);
+    else
+        launch_tile<256, 256, 4, 2, 2, false>(p, p.resident, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.part_planes) return e;
     const int64_t groups = (((int64_t)p.M + 15) / 16) * (((int64_t)p.N + 127) / 128);

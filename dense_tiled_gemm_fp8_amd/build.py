@@ -28,6 +28,13 @@ HIPCC_FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 
+# flags of single files
+FILE_FLAGS = {
+    # sums of matrix instructions go through vector instructions, which cannot
+    # read accumulation registers
+    "block.hip": ["-mllvm", "--amdgpu-mfma-vgpr-form=1"],
+}
+
 
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
@@ -38,8 +45,8 @@ def hipcc() -> str:
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-c",
-                                     os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc()] + HIPCC_FLAGS + FILE_FLAGS.get(src, []) + ["-I", os.path.join(ROOT, "include"), "-c",
+                                                              os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("hipcc failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
@@ -65,8 +72,8 @@ def device_asm(src: str = "kernels.hip") -> str:
     """AMD GCN assembly of our own device code (for instruction-mix checks)."""
     os.makedirs(BUILD, exist_ok=True)
     out = os.path.join(BUILD, os.path.splitext(src)[0] + ".s")
-    cmd = [hipcc()] + HIPCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "--cuda-device-only",
-                                     "-S", os.path.join(CSRC, src), "-o", out]
+    cmd = [hipcc()] + HIPCC_FLAGS + FILE_FLAGS.get(src, []) + ["-I", os.path.join(ROOT, "include"), "--cuda-device-only",
+                                                              "-S", os.path.join(CSRC, src), "-o", out]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("hipcc -S failed:\n%s%s" % (r.stdout, r.stderr))

@@ -293,24 +293,27 @@ __device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b)
     b = r[1];
 }
 
+/* Quads FROM .. FROM + QUADS - 1 as the first columns. */
+template <int FROM, int QUADS>
 __device__ __forceinline__ void store_part(const BlockGemmParams &p, float *plane, const Place &at, const f32x16 &v)
 {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < QUADS; ++q) {
         const int32_t n = at.n + 8 * q + 4 * at.h;
         f32x4 t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = v[4 * q + e];
+        for (int e = 0; e < 4; ++e) t[e] = v[4 * (FROM + q) + e];
         if (at.m < p.M && n < p.N) *(f32x4 *)(plane + (int64_t)at.m * p.ldp + n) = t;
     }
 }
 
+template <int QUADS>
 __device__ __forceinline__ void store_rows(const BlockGemmParams &p, const Place &at, const f32x16 &v)
 {
     if (p.vec && !p.y_f32) {
         /* 8 columns a lane: quads 0 and 1 (2 and 3) of both halves trade places */
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
+        for (int q = 0; q < QUADS; q += 2) {
             uint32_t d[2][2];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -335,7 +338,7 @@ __device__ __forceinline__ void store_rows(const BlockGemmParams &p, const Place
         return;
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < QUADS; ++q) {
         f32x4 t;
 #pragma unroll
         for (int e = 0; e < 4; ++e) t[e] = v[4 * q + e];
@@ -373,17 +376,18 @@ __device__ __forceinline__ void store_codes(const BlockGemmParams &p, const Plac
 /*
  * TX tokens and TW rows of w (of two matrices: TW / 2 of each, of the same columns)
  * a tile, a workgroup of WX x WW wavefronts, one K block of 128 a stage of a ring of
- * two.  A wavefront's block is two by FW matrix blocks of 32 x 32, in a row of two
+ * ST.  A wavefront's block is two by FW matrix blocks of 32 x 32, in a row of two
  * at a time: the sums of a K block come from two instructions each, begun at zero,
  * and the multiply-adds of them into the fp32 sums run while the matrix unit has the
  * instruction behind: the first's during the second's, the second's during the next
  * row's first.  Fragments are read into their own registers again right after their
- * last use.
+ * last use.  (FW = 1, for few tokens: the fragments of two K blocks are held, and
+ * the sums of two, so that neither LDS nor the multiply-adds are waited for.)
  *
  * A stage is rows of 128 bytes (a row's 16-byte unit c lies at c ^ (row / 2 % 8)),
  * the tokens' scales and the weights'.  Before the last row of matrix blocks of a K
  * block is a barrier: by then every fragment of the stage has been read and the
- * next stage has landed, and the weights' copies of the K block two ahead follow it.
+ * next stage has landed, and the weights' copies of the K block ST ahead follow it.
  * The tokens' fragments have been read by all one row earlier (FW > 2: a second
  * barrier, before row 1), and the tokens' copies go there, so that the copies of a
  * K block come in two bursts.
@@ -392,18 +396,20 @@ __device__ __forceinline__ void store_codes(const BlockGemmParams &p, const Plac
  * of its next unit land before it stores the sums of this one, from registers, and
  * nothing waits for the stores before the unit's second K block.
  */
-template <int TX, int TW, int WX, int WW, int MINB, bool TWO, bool EXACT>
+template <int TX, int TW, int WX, int WW, int ST, int MINB, bool TWO, bool EXACT>
 __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemmParams p)
 {
     constexpr int NW = WX * WW, WTX = TX / WX, WTW = TW / WW, FX = WTX / 32, FW = WTW / 32;
     constexpr int XB = TX * 128, WB = TW * 128, SCX = XB + WB, SCW = SCX + TX * 4, STAGE = SCW + 256;
-    constexpr int XL = TX / 8 / NW, WL = TW / 8 / NW, LOADS = XL + WL + 1;
-    constexpr int OC = TWO ? WTW / 2 : WTW, OF = OC / 32, TN = TWO ? TW / 2 : TW;   /* columns out */
-    constexpr int SCG = TX / 64 + 1;               /* scale copies of a stage */
+    constexpr int SCG = TX / 64 + 1, SL = (SCG + NW - 1) / NW;       /* scale copies of a stage, of a wavefront */
+    constexpr int XL = TX / 8 / NW, WL = TW / 8 / NW, LOADS = XL + WL + SL;
+    constexpr int OC = TWO ? WTW / 2 : WTW, TN = TWO ? TW / 2 : TW;  /* columns out */
+    constexpr int OF = OC < 32 ? 1 : OC / 32, QUADS = OC < 32 ? 2 : 4;
     constexpr bool EARLY = FW > 2;                 /* tokens' copies in row 1 */
-    static_assert(FX == 2 && NW >= SCG && NW % 2 == 0 && WTW <= 128 && LOADS < 64, "tile");
-    static_assert(!TWO || (NW * 8 == WTW / 2), "a copy is of one matrix");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE + WW * TX * 4];
+    constexpr bool HALVES = TWO && FW == 1;        /* both matrices in one matrix block */
+    static_assert(FX == 2 && NW % 2 == 0 && WTW <= 128 && (ST - 1) * LOADS < 64 && (!EARLY || ST == 2), "tile");
+    static_assert(!TWO || OC % (NW * 8) == 0 || (HALVES && NW * 8 % WTW == 0), "a copy is of one matrix");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[ST * STAGE + (TWO && TN == 128 ? WW * TX * 4 : 0)];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wx = wave / WW, ww = wave % WW;
@@ -411,14 +417,19 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
     const uint32_t base = lds_addr(smem);
     /* the scale copies of a stage go round the wavefronts (those past the last
      * repeat the first: the same values to the same place) */
-    const int sg = wave % SCG;
-    const int64_t sc_step = sg < SCG - 1 ? p.lxs : 1;
+    int sg[SL];
+    int64_t sc_step[SL];
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+        sg[i] = (wave + i * NW) % SCG;
+        sc_step[i] = sg[i] < SCG - 1 ? p.lxs : 1;
+    }
 
     /* the unit in hand, and what its copies need of a lane */
     int32_t m0, n0, part, k0, k1, have;
     i32x4 rx, rw, ru;
     uint32_t xoff[XL], woff[WL];
-    const float *sc;
+    const float *sc[SL];
     int lane, unit;
     auto setup = [&](int32_t id) __attribute__((always_inline)) {
         /* formed from a lane index that the compiler cannot see through, or it
@@ -440,6 +451,8 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
         rx = rsrc_words(p.x + (int64_t)m0 * p.ldx);
         rw = rsrc_words(p.w + (int64_t)n0 * p.ldw);
         if constexpr (TWO) ru = rsrc_words(p.up + (int64_t)n0 * p.ldu);
+        const bool second = HALVES && wave * 8 % WTW >= OC;       /* this wavefront copies up */
+        if (second) rw = ru;
 #pragma unroll
         for (int d = 0; d < XL; ++d) {
             const int r = (d * NW + wave) * 8 + drow;
@@ -449,16 +462,20 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
         for (int d = 0; d < WL; ++d) {
             int r = (d * NW + wave) * 8 + drow;
             if constexpr (TWO) r = r / WTW * OC + r % OC;
-            woff[d] = n0 + r < p.N ? (uint32_t)(r * (int32_t)(TWO && (d & 1) ? p.ldu : p.ldw) + unit * 16) : kOOB;
+            const bool u = HALVES ? second : TWO && (d * NW * 8 / OC) % 2 == 1;
+            woff[d] = n0 + r < p.N ? (uint32_t)(r * (int32_t)(u ? p.ldu : p.ldw) + unit * 16) : kOOB;
         }
         /* rows past the last repeat its scale */
-        if (sg < SCG - 1)
-            sc = p.xs + std::min(m0 + sg * 64 + lane, p.M - 1);
-        else if (TWO)
-            sc = lane & 1 ? p.us + (int64_t)(n0 >> 7) * p.lus : p.ws + (int64_t)(n0 >> 7) * p.lws;
-        else
-            sc = p.ws + (int64_t)(std::min(n0 + (lane & 1) * 128, p.N - 1) >> 7) * p.lws;
-        sc += k0 * sc_step;
+#pragma unroll
+        for (int i = 0; i < SL; ++i) {
+            if (sg[i] < SCG - 1)
+                sc[i] = p.xs + std::min(m0 + sg[i] * 64 + lane, p.M - 1);
+            else if (TWO)
+                sc[i] = lane & 1 ? p.us + (int64_t)(n0 >> 7) * p.lus : p.ws + (int64_t)(n0 >> 7) * p.lws;
+            else
+                sc[i] = p.ws + (int64_t)(std::min(n0 + (lane & 1) * 128, p.N - 1) >> 7) * p.lws;
+            sc[i] += k0 * sc_step[i];
+        }
         /* K blocks whose unit of this lane lies before K, in this part */
         have = std::min(k1, (p.K - unit * 16 + 127) >> 7);
     };
@@ -469,17 +486,20 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
         if constexpr (d < XL) {
             dma16<d * NW * 1024>(rx, base + so + wave * 1024, kb < have ? xoff[d] + k : kOOB);
         } else if constexpr (d < XL + WL) {
-            dma16<XB + (d - XL) * NW * 1024>(TWO && ((d - XL) & 1) ? ru : rw, base + so + wave * 1024,
+            dma16<XB + (d - XL) * NW * 1024>(TWO && !HALVES && ((d - XL) * NW * 8 / OC) % 2 == 1 ? ru : rw, base + so + wave * 1024,
                                              kb < have ? woff[d - XL] + k : kOOB);
         } else {
-            dma_global4(base + so + SCX + sg * 256, sc);
-            if (kb + 1 < k1) sc += sc_step;
+            constexpr int i = d - XL - WL;
+            dma_global4(base + so + SCX + sg[i] * 256, sc[i]);
+            if (kb + 1 < k1) sc[i] += sc_step[i];
         }
     };
     auto first_copies = [&]() __attribute__((always_inline)) {
         if (k1 <= k0) return;
-        unroll<LOADS>([&](auto dc) __attribute__((always_inline)) { copy(dc, k0, 0u); });
-        unroll<LOADS>([&](auto dc) __attribute__((always_inline)) { copy(dc, k0 + 1, (uint32_t)STAGE); });
+        unroll<ST>([&](auto tc) __attribute__((always_inline)) {
+            constexpr int t = decltype(tc)::value;
+            unroll<LOADS>([&](auto dc) __attribute__((always_inline)) { copy(dc, k0 + t, (uint32_t)(t * STAGE)); });
+        });
     };
     /* K ends inside a unit: the lanes that copied it clear what lies behind, once it
      * has landed */
@@ -503,8 +523,8 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
     if (id >= units) return;
     setup(id);
     first_copies();
-    if (k1 > k0) wait_vmcnt<LOADS>();
-    bool both = false;            /* the first two K blocks have landed */
+    if (k1 > k0) wait_vmcnt<(ST - 1) * LOADS>();
+    int ahead = 0;                /* K blocks that need no wait: they have landed */
     for (;;) {
         f32x16 acc[FW][2];
 #pragma unroll
@@ -520,125 +540,233 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
                 const i32x4 hi = *(const i32x4 *)(row + (((4 * s + 2 * h + 1) ^ sw) << 4));
                 return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             };
-            i32x8 xf[2][2], wf[2];
-            float sx[2], sw_[2];
-            auto read_w = [&](uint32_t so, int f, int s) __attribute__((always_inline)) {
-                wf[s] = frag(so + XB + (ww * WTW + f * 32) * 128, s);
-            };
-            auto read_x = [&](uint32_t so, int x, int s) __attribute__((always_inline)) {
-                xf[x][s] = frag(so + (wx * WTX + x * 32) * 128, s);
-            };
-            auto read_scales = [&](uint32_t so) __attribute__((always_inline)) {
+            if constexpr (FW == 1) {
+                /* both K blocks' fragments in registers: a K block's are read while the
+                 * one before it is multiplied */
+                i32x8 xf[2][2][2], wf[2][2];
+                float sx[2][2], sw_[2][2], by[2][2];
+                f32x16 sum[2][2];
+                auto read = [&](auto bc, uint32_t so, int part) __attribute__((always_inline)) {
+                    constexpr int b = decltype(bc)::value;
+                    if (part < 2) {
+                        wf[b][part] = frag(so + XB + ww * WTW * 128, part);
+                        xf[b][0][part] = frag(so + wx * WTX * 128, part);
+                        return;
+                    }
+                    xf[b][1][part - 2] = frag(so + (wx * WTX + 32) * 128, part - 2);
+                    if (part == 3) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) sx[x] = *(const float *)(smem + so + SCX + (wx * WTX + x * 32 + frow) * 4);
-                sw_[0] = *(const float *)(smem + so + SCW + (TWO ? 0 : ww * WTW / 128 * 4));
-                sw_[1] = TWO ? *(const float *)(smem + so + SCW + 4) : 0.0f;
-            };
-
-            /* the unit's first K block has landed */
-            clear_tail(k0, 0);
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
+                        for (int x = 0; x < 2; ++x) sx[b][x] = *(const float *)(smem + so + SCX + (wx * WTX + x * 32 + frow) * 4);
+                        sw_[b][0] = *(const float *)(smem + so + SCW + (TWO ? 0 : ww * WTW / 128 * 4));
+                        sw_[b][1] = TWO ? *(const float *)(smem + so + SCW + 4) : 0.0f;
+                    }
+                };
+                auto multiply = [&](auto bc, int x, int s) __attribute__((always_inline)) {
+                    constexpr int b = decltype(bc)::value;
+                    f32x16 v = s ? sum[b][x] : f32x16{};
+                    if constexpr (EXACT) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                read_x(0, 0, s);
-                read_x(0, 1, s);
-                read_w(0, 0, s);
-            }
-            read_scales(0);
-
-            f32x16 sum[2];
-            float scale[2][2], last = 0.0f;
-            sum[0] = sum[1] = f32x16{};
-            uint32_t so = 0;
-            auto multiply = [&](int x, int s) __attribute__((always_inline)) {
-                f32x16 v = s ? sum[x] : f32x16{};
-                if constexpr (EXACT) {
+                        for (int i = 0; i < 4; ++i)
+                            v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(wf[b][s], i), widen(xf[b][x][s], i), v, 0, 0, 0);
+                    } else {
+                        v = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[b][s], xf[b][x][s], v, 0, 0, 0, 0, 0, 0);
+                    }
+                    sum[b][x] = v;
+                };
+                auto add = [&](auto bc, int x) __attribute__((always_inline)) {
+                    constexpr int b = decltype(bc)::value;
+                    const float s0 = by[0][x], s1 = by[1][x];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(wf[s], i), widen(xf[x][s], i), v, 0, 0, 0);
-                } else {
-                    v = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[s], xf[x][s], v, 0, 0, 0, 0, 0, 0);
+                    for (int e = 0; e < 16; ++e) acc[0][x][e] = __builtin_fmaf(sum[b][x][e], HALVES && e >= 8 ? s1 : s0, acc[0][x][e]);
+                    asm volatile("" : "+v"(acc[0][x]));
+                };
+                auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
+                typedef std::integral_constant<int, 0> Zero;
+                typedef std::integral_constant<int, 1> One;
+                clear_tail(k0, 0);
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) read(Zero{}, 0, i);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    sum[1][x] = f32x16{};
+                    by[0][x] = by[1][x] = 0.0f;
                 }
-                sum[x] = v;
-            };
-            auto add = [&](f32x16 &a, int x, float by) __attribute__((always_inline)) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) a[e] = __builtin_fmaf(sum[x][e], by, a[e]);
-                /* here, not where the sums are next used */
-                asm volatile("" : "+v"(a));
-            };
-            auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
-            for (int32_t kb = k0; kb < k1; ++kb) {
-                const uint32_t next = so ^ (uint32_t)STAGE;
-                unroll<FW>([&](auto fc) __attribute__((always_inline)) {
-                    constexpr int f = decltype(fc)::value;
-                    constexpr bool end = f == FW - 1;
-                    constexpr int m = TWO && f >= FW / 2 ? 1 : 0;
-                    /* this row's copies: a quarter behind each instruction */
-                    constexpr int c0 = EARLY && end ? XL : 0, c1 = EARLY ? f == 1 ? XL : end ? LOADS : 0 : end ? LOADS : 0;
+                uint32_t so = 0;
+                auto block = [&](auto bc, int32_t kb) __attribute__((always_inline)) {
+                    constexpr int b = decltype(bc)::value;
+                    typedef std::integral_constant<int, 1 - b> Other;
+                    const uint32_t next = so + STAGE == ST * STAGE ? 0 : so + STAGE;
                     auto copies = [&](auto qc) __attribute__((always_inline)) {
                         constexpr int q = decltype(qc)::value;
                         unroll<LOADS>([&](auto dc) __attribute__((always_inline)) {
-                            constexpr int d = decltype(dc)::value;
-                            if constexpr (d >= c0 && d < c1 && (d - c0) * 4 / (c1 - c0) == q) copy(dc, kb + 2, so);
+                            if constexpr (decltype(dc)::value * 4 / LOADS == q) copy(dc, kb + ST, so);
                         });
                     };
-                    if constexpr (EARLY && f == 1) {
-                        __builtin_amdgcn_s_barrier();
-                        asm volatile("" ::: "memory");
-                    }
-                    if constexpr (end) {
-                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                        /* (of a workgroup's later units the first two have landed
-                         * before: stores of the unit before are not waited for yet) */
-                        if (!both) wait_vmcnt<EARLY ? XL : 0>();
-                        both = false;
-                        clear_tail(kb + 1, next);
-                        __builtin_amdgcn_s_barrier();
-                        asm volatile("" ::: "memory");
-                    }
-                    multiply(0, 0);
-                    fence();
-                    if constexpr (end) read_x(next, 0, 0);
-                    copies(std::integral_constant<int, 0>{});
-                    /* the row before: of the K block before for the first */
-                    add(acc[f == 0 ? FW - 1 : f - 1][1], 1, f == 0 ? last : scale[TWO && f - 1 >= FW / 2 ? 1 : 0][1]);
-                    fence();
-                    multiply(1, 0);
-                    fence();
-                    if constexpr (f == 0) {
-                        /* not before: their reads were the last ones */
+                    /* this K block's fragments are here, from every wavefront's view:
+                     * its stage is free, and the next has landed */
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    if (ahead > 0)
+                        --ahead;
+                    else
+                        wait_vmcnt<(ST - 2) * LOADS>();
+                    clear_tail(kb + 1, next);
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    unroll<4>([&](auto ic) __attribute__((always_inline)) {
+                        constexpr int i = decltype(ic)::value;
+                        multiply(bc, i & 1, i >> 1);
+                        fence();
+                        read(Other{}, next, i);
+                        copies(ic);
+                        if constexpr (i >= 2) add(Other{}, i - 2);
+                        fence();
+                    });
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            scale[0][x] = sx[x] * sw_[0];
-                            if (TWO) scale[1][x] = sx[x] * sw_[1];
+                    for (int x = 0; x < 2; ++x) {
+                        by[0][x] = sx[b][x] * sw_[b][0];
+                        by[1][x] = sx[b][x] * sw_[b][1];
+                    }
+                    so = next;
+                };
+                int32_t kb = k0;
+                for (; kb + 1 < k1; kb += 2) {
+                    block(Zero{}, kb);
+                    block(One{}, kb + 1);
+                }
+                if (kb < k1) {
+                    block(Zero{}, kb);
+                    add(Zero{}, 0);
+                    add(Zero{}, 1);
+                } else {
+                    add(One{}, 0);
+                    add(One{}, 1);
+                }
+            } else {
+                i32x8 xf[2][2], wf[2];
+                float sx[2], sw_[2];
+                auto read_w = [&](uint32_t so, int f, int s) __attribute__((always_inline)) {
+                    wf[s] = frag(so + XB + (ww * WTW + f * 32) * 128, s);
+                };
+                auto read_x = [&](uint32_t so, int x, int s) __attribute__((always_inline)) {
+                    xf[x][s] = frag(so + (wx * WTX + x * 32) * 128, s);
+                };
+                auto read_scales = [&](uint32_t so) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) sx[x] = *(const float *)(smem + so + SCX + (wx * WTX + x * 32 + frow) * 4);
+                    sw_[0] = *(const float *)(smem + so + SCW + (TWO ? 0 : ww * WTW / 128 * 4));
+                    sw_[1] = TWO ? *(const float *)(smem + so + SCW + 4) : 0.0f;
+                };
+
+                /* the unit's first K block has landed */
+                clear_tail(k0, 0);
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    read_x(0, 0, s);
+                    read_x(0, 1, s);
+                    read_w(0, 0, s);
+                }
+                read_scales(0);
+
+                f32x16 sum[2];
+                float scale[2][2], last = 0.0f, last2 = 0.0f;
+                sum[0] = sum[1] = f32x16{};
+                uint32_t so = 0;
+                auto multiply = [&](int x, int s) __attribute__((always_inline)) {
+                    f32x16 v = s ? sum[x] : f32x16{};
+                    if constexpr (EXACT) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(wf[s], i), widen(xf[x][s], i), v, 0, 0, 0);
+                    } else {
+                        v = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[s], xf[x][s], v, 0, 0, 0, 0, 0, 0);
+                    }
+                    sum[x] = v;
+                };
+                auto add = [&](f32x16 &a, int x, float by, float by2) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) a[e] = __builtin_fmaf(sum[x][e], HALVES && e >= 8 ? by2 : by, a[e]);
+                    /* here, not where the sums are next used */
+                    asm volatile("" : "+v"(a));
+                };
+                auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
+                for (int32_t kb = k0; kb < k1; ++kb) {
+                    const uint32_t next = so + STAGE == ST * STAGE ? 0 : so + STAGE;
+                    unroll<FW>([&](auto fc) __attribute__((always_inline)) {
+                        constexpr int f = decltype(fc)::value;
+                        constexpr bool end = f == FW - 1;
+                        constexpr int m = TWO && !HALVES && f >= FW / 2 ? 1 : 0;
+                        /* this row's copies: a quarter behind each instruction */
+                        constexpr int c0 = EARLY && end ? XL : 0, c1 = EARLY ? f == 1 ? XL : end ? LOADS : 0 : end ? LOADS : 0;
+                        auto copies = [&](auto qc) __attribute__((always_inline)) {
+                            constexpr int q = decltype(qc)::value;
+                            unroll<LOADS>([&](auto dc) __attribute__((always_inline)) {
+                                constexpr int d = decltype(dc)::value;
+                                if constexpr (d >= c0 && d < c1 && (d - c0) * 4 / (c1 - c0) == q) copy(dc, kb + ST, so);
+                            });
+                        };
+                        if constexpr (EARLY && f == 1) {
+                            __builtin_amdgcn_s_barrier();
+                            asm volatile("" ::: "memory");
                         }
-                    }
-                    read_w(end ? next : so, end ? 0 : f + 1, 0);
-                    if constexpr (end) read_x(next, 1, 0);
-                    copies(std::integral_constant<int, 1>{});
-                    fence();
-                    multiply(0, 1);
-                    fence();
-                    if constexpr (end) read_x(next, 0, 1);
-                    copies(std::integral_constant<int, 2>{});
-                    fence();
-                    multiply(1, 1);
-                    fence();
-                    read_w(end ? next : so, end ? 0 : f + 1, 1);
-                    if constexpr (end) {
-                        read_x(next, 1, 1);
-                        read_scales(next);
-                    }
-                    copies(std::integral_constant<int, 3>{});
-                    add(acc[f][0], 0, scale[m][0]);
-                    fence();
-                });
-                last = scale[TWO ? 1 : 0][1];
-                so = next;
+                        if constexpr (end) {
+                            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                            /* (of a workgroup's later units the first ST have landed
+                             * before: stores of the unit before are not waited for yet) */
+                            if (ahead > 0)
+                                --ahead;
+                            else
+                                wait_vmcnt<(ST - 2) * LOADS + (EARLY ? XL : 0)>();
+                            clear_tail(kb + 1, next);
+                            __builtin_amdgcn_s_barrier();
+                            asm volatile("" ::: "memory");
+                        }
+                        multiply(0, 0);
+                        fence();
+                        if constexpr (end) read_x(next, 0, 0);
+                        copies(std::integral_constant<int, 0>{});
+                        /* the row before: of the K block before for the first */
+                        add(acc[f == 0 ? FW - 1 : f - 1][1], 1, f == 0 ? last : scale[TWO && f - 1 >= FW / 2 ? 1 : 0][1], last2);
+                        fence();
+                        multiply(1, 0);
+                        fence();
+                        if constexpr (f == 0) {
+                            /* not before: their reads were the last ones */
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                scale[0][x] = sx[x] * sw_[0];
+                                if (TWO) scale[1][x] = sx[x] * sw_[1];
+                            }
+                        }
+                        read_w(end ? next : so, end ? 0 : f + 1, 0);
+                        if constexpr (end) read_x(next, 1, 0);
+                        copies(std::integral_constant<int, 1>{});
+                        fence();
+                        multiply(0, 1);
+                        fence();
+                        if constexpr (end) read_x(next, 0, 1);
+                        copies(std::integral_constant<int, 2>{});
+                        fence();
+                        multiply(1, 1);
+                        fence();
+                        read_w(end ? next : so, end ? 0 : f + 1, 1);
+                        if constexpr (end) {
+                            read_x(next, 1, 1);
+                            read_scales(next);
+                        }
+                        copies(std::integral_constant<int, 3>{});
+                        add(acc[f][0], 0, scale[m][0], scale[TWO ? 1 : 0][0]);
+                        fence();
+                    });
+                    last = scale[TWO && !HALVES ? 1 : 0][1];
+                    if (HALVES) last2 = scale[1][1];
+                    so = next;
+                }
+                add(acc[FW - 1][1], 1, last, last2);
             }
-            add(acc[FW - 1][1], 1, last);
         }
 
         /* every fragment has been read and the copies of K blocks past the last have
@@ -666,8 +794,8 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float a = acc[f][x][e], b = acc[OF + f][x][e];
+                        for (int e = 0; e < 4 * QUADS; ++e) {
+                            const float a = acc[f][x][e], b = HALVES ? acc[f][x][8 + e] : acc[(OF + f) % FW][x][e];
                             acc[f][x][e] = gated(a, b, p.act);
                         }
                         __builtin_amdgcn_sched_barrier(0);
@@ -676,7 +804,7 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
         }
         if (more) {
             wait_vmcnt<0>();
-            both = true;
+            ahead = ST - 1;
         }
         if (p.part_planes) {
             const int64_t plane = (int64_t)p.M * p.ldp;
@@ -686,14 +814,15 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
 #pragma unroll
                 for (int f = 0; f < OF; ++f) {
                     const Place at{mw + x * 32 + (el & 31), nw + f * 32, h};
-                    store_part(p, o, at, acc[f][x]);
+                    store_part<0, QUADS>(p, o, at, acc[f][x]);
                     if constexpr (TWO)
-                        if (!activate) store_part(p, o + plane, at, acc[OF + f][x]);
+                        if (!activate) store_part<HALVES ? 2 : 0, QUADS>(p, o + plane, at, acc[(OF + f) % FW][x]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-        } else if (TWO && p.q.codes) {
+        } else if (TWO && TN == 128 && p.q.codes) {
+            if constexpr (TWO && TN == 128) {
             /* a row's 128 columns are those of the WW wavefronts beside each other */
-            float *red = (float *)(smem + 2 * STAGE);
+            float *red = (float *)(smem + ST * STAGE);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float a = 0.0f;
@@ -725,12 +854,13 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
+            }
         } else {
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int f = 0; f < OF; ++f) {
-                    store_rows(p, Place{mw + x * 32 + (el & 31), nw + f * 32, h}, acc[f][x]);
+                    store_rows<QUADS>(p, Place{mw + x * 32 + (el & 31), nw + f * 32, h}, acc[f][x]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
         }
@@ -795,6 +925,16 @@ __global__ __launch_bounds__(256) void block_finish_kernel(BlockGemmParams p)
     for (int j = 0; n + j < p.N; ++j) c[j] = (uint8_t)((uint32_t)w[j >> 2] >> (8 * (j & 3)));
 }
 
+namespace {
+
+/* Tiles: tokens, rows of w, K blocks in the ring, workgroups a compute unit. */
+struct Form {
+    int32_t tx, tw, st, resident;
+};
+constexpr Form kForms[] = {{16, 32, 3, 1}, {64, 32, 3, 1}, {128, 128, 2, 2}, {256, 256, 2, 1}, {128, 128, 4, 1}, {128, 64, 6, 1}, {128, 32, 6, 1}, {64, 128, 6, 1}, {128, 128, 4, 1}};
+
+} /* namespace */
+
 int64_t block_plan(BlockGemmParams &p, int32_t splits, int32_t cus)
 {
     p.exact = p.y && p.y_f32;
@@ -804,10 +944,11 @@ int64_t block_plan(BlockGemmParams &p, int32_t splits, int32_t cus)
     if (p.form == 3 && p.exact) p.form = 2;
     int64_t units = 1;
     if (p.form >= 2) {
-        const int32_t tx = p.form == 2 ? 128 : 256, tn = (p.form == 2 ? 128 : 256) >> p.two;
-        units = ((int64_t)p.M + tx - 1) / tx * (((int64_t)p.N + tn - 1) / tn);
+        const Form &f = kForms[p.form];
+        const int32_t tn = f.tw >> p.two;
+        units = ((int64_t)p.M + f.tx - 1) / f.tx * (((int64_t)p.N + tn - 1) / tn);
+        p.resident = f.resident * cus;
     }
-    p.resident = p.form == 2 ? 2 * cus : cus;
     p.splits = std::max(1, std::min({splits, p.nk, 256}));
     /* a scale of codes needs 128 columns in one workgroup */
     p.part_planes = p.splits > 1 ? 1 + p.two : p.q.codes && p.form != 3 ? 1 : 0;
@@ -833,32 +974,36 @@ void launch_rows(const BlockGemmParams &p, hipStream_t stream)
         hipLaunchKernelGGL((block_rows_kernel<FX, 2, NW, ST, false, false>), grid, block, 0, stream, p);
 }
 
-template <int TX, int TW, int WX, int WW, int MINB, bool EXACT>
-void launch_tile(const BlockGemmParams &p, int64_t most, hipStream_t stream)
+template <int FORM, int WX, int WW, int MINB, bool EXACT>
+void launch_tile(const BlockGemmParams &p, hipStream_t stream)
 {
+    constexpr int TX = kForms[FORM].tx, TW = kForms[FORM].tw, ST = kForms[FORM].st;
     const int64_t tn = p.two ? TW / 2 : TW;
     const int64_t units = (((int64_t)p.M + TX - 1) / TX) * ((p.N + tn - 1) / tn) * p.splits;
-    const dim3 grid((uint32_t)std::min(units, most)), block(WX * WW * 64);
-    if (p.two)
-        hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, MINB, true, EXACT>), grid, block, 0, stream, p);
-    else
-        hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, MINB, false, EXACT>), grid, block, 0, stream, p);
+    const dim3 grid((uint32_t)std::min<int64_t>(units, p.resident)), block(WX * WW * 64);
+    if constexpr (TW > 32)
+        if (p.two) {
+            hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, ST, MINB, true, EXACT>), grid, block, 0, stream, p);
+            return;
+        }
+    hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, ST, MINB, false, EXACT>), grid, block, 0, stream, p);
 }
 
 } /* namespace */
 
 hipError_t launch_block_gemm(const BlockGemmParams &p, hipStream_t stream)
 {
-    if (p.form == 0)
-        launch_rows<1, 8, 3>(p, stream);
-    else if (p.form == 1)
-        launch_rows<4, 4, 3>(p, stream);
-    else if (p.form == 2 && p.exact)
-        launch_tile<128, 128, 2, 2, 2, true>(p, p.resident, stream);
-    else if (p.form == 2)
-        launch_tile<128, 128, 2, 2, 2, false>(p, p.resident, stream);
-    else
-        launch_tile<256, 256, 4, 2, 2, false>(p, p.resident, stream);
+    switch (p.form) {
+    case 0: launch_rows<1, 8, 3>(p, stream); break;
+    case 1: launch_rows<4, 4, 3>(p, stream); break;
+    case 2: p.exact ? launch_tile<2, 2, 2, 2, true>(p, stream) : launch_tile<2, 2, 2, 2, false>(p, stream); break;
+    case 3: launch_tile<3, 4, 2, 2, false>(p, stream); break;
+    case 4: p.exact ? launch_tile<4, 2, 2, 1, true>(p, stream) : launch_tile<4, 2, 2, 1, false>(p, stream); break;
+    case 5: p.exact ? launch_tile<5, 2, 2, 1, true>(p, stream) : launch_tile<5, 2, 2, 1, false>(p, stream); break;
+    case 6: p.exact ? launch_tile<6, 2, 1, 1, true>(p, stream) : launch_tile<6, 2, 1, 1, false>(p, stream); break;
+    case 8: p.exact ? launch_tile<8, 2, 4, 2, true>(p, stream) : launch_tile<8, 2, 4, 2, false>(p, stream); break;
+    default: p.exact ? launch_tile<7, 1, 4, 1, true>(p, stream) : launch_tile<7, 1, 4, 1, false>(p, stream); break;
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.part_planes) return e;
     const int64_t groups = (((int64_t)p.M + 15) / 16) * (((int64_t)p.N + 127) / 128);

@@ -868,6 +868,227 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
     }
 }
 
+/*
+ * Some tokens, a stream of weights: 128 tokens and 32 rows of w (of two matrices 16 of
+ * each) a workgroup.  Memory answers after some 2 us, the caches, where x comes from,
+ * after less than one, and a wavefront's copies land in order: so they are made by
+ * wavefronts of their own, two that keep a ring of XS steps of x filled and one for a
+ * ring of WS of w.  Four multiply, 32 tokens each.  A step is B K blocks, whose
+ * fragments are read while the step before is multiplied; all meet at one barrier a
+ * step.
+ */
+template <int B, int XS, int WS, bool TWO, bool EXACT>
+__global__ __launch_bounds__(448) void block_stream_kernel(BlockGemmParams p)
+{
+    constexpr int TX = 128;
+    constexpr int XBLOCK = TX * 128 + TX * 4, WBLOCK = 4096 + 256, W0 = XS * B * XBLOCK;
+    constexpr int XL = TX / 16;                             /* copies of a block's rows */
+    static_assert(XS >= 2 && WS >= 2 && (XS - 1) * B * (XL + 1) < 64 && (WS - 1) * B * 5 < 64, "rings");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[W0 + WS * B * WBLOCK];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+    constexpr int COLS = TWO ? 16 : 32;
+    const int32_t n0 = blockIdx.x * COLS, m0 = blockIdx.y * TX, part = blockIdx.z;
+    const int32_t k0 = kslice_begin(p.nk, p.splits, part), k1 = kslice_begin(p.nk, p.splits, part + 1);
+    const int32_t steps = (k1 - k0 + B - 1) / B;
+    const uint32_t base = lds_addr(smem);
+
+    if (wave >= 4) {
+        /* copies: 8 rows each, the lane's row and the 16-byte unit that belongs at its
+         * place, c ^ (row / 2 % 8) */
+        const int drow = lane >> 3, pw = wave - 4;
+        int32_t unit[2], have[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            unit[e] = (lane & 7) ^ ((4 * e + (drow >> 1)) & 7);
+            have[e] = std::min(k1, (p.K - unit[e] * 16 + 127) >> 7);
+        }
+        auto stream = [&](auto is_w) __attribute__((always_inline)) {
+            constexpr bool W = decltype(is_w)::value;
+            constexpr int N = W ? 4 : XL, RING = W ? WS : XS, BLOCK = W ? WBLOCK : XBLOCK, LOADS = B * (N + 1);
+            const uint8_t *from = W ? p.w + (int64_t)n0 * p.ldw : p.x + (int64_t)m0 * p.ldx;
+            const i32x4 r0 = rsrc_words(from), r1 = rsrc_words(W && TWO ? p.up + (int64_t)n0 * p.ldu : from);
+            uint32_t off[N];
+#pragma unroll
+            for (int d = 0; d < N; ++d) {
+                const int r = (W ? (TWO ? d & 1 : d) : pw * N + d) * 8 + drow;
+                const bool in = W ? n0 + r < p.N : m0 + r < p.M;
+                off[d] = in ? (uint32_t)(r * (int32_t)(W ? (TWO && d >= 2 ? p.ldu : p.ldw) : p.ldx) + unit[d & 1] * 16) : kOOB;
+            }
+            /* scales: of w the lanes of an odd index take the second matrix's, of x each
+             * of the two wavefronts 64 tokens'; rows past the last repeat its, blocks
+             * past the last too (their codes are zeros) */
+            const float *sc;
+            if (W)
+                sc = TWO && (lane & 1) ? p.us + (int64_t)(n0 >> 7) * p.lus : p.ws + (int64_t)(n0 >> 7) * p.lws;
+            else
+                sc = p.xs + std::min(m0 + pw * 64 + lane, p.M - 1);
+            const int64_t step = W ? 1 : p.lxs;
+            sc += k0 * step;
+            const uint32_t ring = W ? W0 : 0, rows = W ? 0 : pw * N * 1024, scales = W ? 4096 : TX * 128 + pw * 256;
+            auto copy = [&](int32_t kb, uint32_t so) __attribute__((always_inline)) {
+                unroll<B>([&](auto jc) __attribute__((always_inline)) {
+                    constexpr int j = decltype(jc)::value;
+                    unroll<N>([&](auto dc) __attribute__((always_inline)) {
+                        constexpr int d = decltype(dc)::value;
+                        dma16<j * BLOCK + d * 1024>(W && TWO && d >= 2 ? r1 : r0, base + ring + so + rows,
+                                                    kb + j < have[d & 1] ? off[d] + (uint32_t)(kb + j) * 128 : kOOB);
+                    });
+                    dma_global4(base + ring + so + j * BLOCK + scales, sc);
+                    if (kb + j + 1 < k1) sc += step;
+                });
+            };
+            /* K ends inside a unit: the lanes that copied it clear what lies behind */
+            auto clear_tail = [&](int32_t kb, uint32_t so) __attribute__((always_inline)) {
+                const int32_t end = p.nk - 1;
+                if ((p.K & 15) == 0 || kb > end || kb + B <= end || end >= k1) return;
+                for (int d = 0; d < N; ++d) {
+                    const int32_t left = p.K - end * 128 - unit[d & 1] * 16;
+                    uint8_t *u = smem + ring + so + (end - kb) * BLOCK + rows + d * 1024 + lane * 16;
+                    for (int b = left; left > 0 && b < 16; ++b) u[b] = 0;
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            };
+            unroll<RING>([&](auto tc) __attribute__((always_inline)) {
+                constexpr int t = decltype(tc)::value;
+                copy(k0 + t * B, (uint32_t)(t * B * BLOCK));
+            });
+            wait_vmcnt<(RING - 1) * LOADS>();
+            clear_tail(k0, 0);
+            __builtin_amdgcn_s_barrier();
+            uint32_t so = 0;
+            for (int32_t i = 0, kb = k0; i < steps; ++i, kb += B) {
+                const uint32_t next = so + B * BLOCK == RING * B * BLOCK ? 0 : so + B * BLOCK;
+                wait_vmcnt<(RING - 2) * LOADS>();
+                clear_tail(kb + B, next);
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                copy(kb + RING * B, so);
+                so = next;
+            }
+            wait_vmcnt<0>();
+        };
+        if (steps > 0) {
+            if (pw == 2)
+                stream(std::true_type{});
+            else
+                stream(std::false_type{});
+        }
+        return;
+    }
+
+    const int wt = wave;                                    /* tokens 32 wt .. */
+    constexpr int S = 2;                                    /* instructions a K block */
+    f32x16 acc{};
+    if (steps > 0) {
+        const int frow = lane & 31, h = lane >> 5, sw = (frow >> 1) & 7;
+        i32x8 xf[2][B][S], wf[2][B][S];
+        float sx[2][B], s0[2][B], s1[2][B], by0[B], by1[B];
+        f32x16 sum[2][B];
+        auto frag = [&](uint32_t rows, int s) __attribute__((always_inline)) {
+            const uint8_t *row = smem + rows + frow * 128;
+            const int c = 4 * s + 2 * h;
+            const i32x4 lo = *(const i32x4 *)(row + ((c ^ sw) << 4));
+            const i32x4 hi = *(const i32x4 *)(row + (((c + 1) ^ sw) << 4));
+            return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        };
+        auto read = [&](int b, uint32_t xo, uint32_t wo) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                const uint32_t xj = xo + j * XBLOCK, wj = W0 + wo + j * WBLOCK;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    wf[b][j][s] = frag(wj, s);
+                    xf[b][j][s] = frag(xj + wt * 4096, s);
+                }
+                sx[b][j] = *(const float *)(smem + xj + TX * 128 + (wt * 32 + frow) * 4);
+                s0[b][j] = *(const float *)(smem + wj + 4096);
+                if (TWO) s1[b][j] = *(const float *)(smem + wj + 4096 + 4);
+            }
+        };
+        auto add = [&](int b, int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = __builtin_fmaf(sum[b][j][e], TWO && e >= 8 ? by1[j] : by0[j], acc[e]);
+            asm volatile("" : "+v"(acc));
+        };
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        read(0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            sum[1][j] = f32x16{};
+            by0[j] = by1[j] = 0.0f;
+        }
+        uint32_t xo = 0, wo = 0;
+        auto block = [&](auto bc) __attribute__((always_inline)) {
+            constexpr int b = decltype(bc)::value;
+            xo = xo + B * XBLOCK == XS * B * XBLOCK ? 0 : xo + B * XBLOCK;
+            wo = wo + B * WBLOCK == WS * B * WBLOCK ? 0 : wo + B * WBLOCK;
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            read(1 - b, xo, wo);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                f32x16 v{};
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    if constexpr (EXACT) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(wf[b][j][s], i), widen(xf[b][j][s], i), v, 0, 0, 0);
+                    } else {
+                        v = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[b][j][s], xf[b][j][s], v, 0, 0, 0, 0, 0, 0);
+                    }
+                }
+                sum[b][j] = v;
+                add(1 - b, j);
+            }
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                by0[j] = sx[b][j] * s0[b][j];
+                if (TWO) by1[j] = sx[b][j] * s1[b][j];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int32_t i = 0;
+        for (; i + 1 < steps; i += 2) {
+            block(std::integral_constant<int, 0>{});
+            block(std::integral_constant<int, 1>{});
+        }
+        if (i < steps) {
+            block(std::integral_constant<int, 0>{});
+#pragma unroll
+            for (int j = 0; j < B; ++j) add(0, j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < B; ++j) add(1, j);
+        }
+    }
+    const Place at{m0 + wt * 32 + (lane & 31), n0, lane >> 5};
+    const int64_t plane = (int64_t)p.M * p.ldp;
+    float *o = p.part + (int64_t)part * p.part_planes * plane;
+    constexpr int QUADS = TWO ? 2 : 4;
+    if (TWO && p.part_planes == 2) {
+        store_part<0, QUADS>(p, o, at, acc);
+        store_part<TWO ? 2 : 0, QUADS>(p, o + plane, at, acc);
+        return;
+    }
+    if constexpr (TWO) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = acc[e], b = acc[8 + e];
+            acc[e] = gated(a, b, p.act);
+        }
+    }
+    if (p.part_planes)
+        store_part<0, QUADS>(p, o, at, acc);
+    else
+        store_rows<QUADS>(p, at, acc);
+}
+
 /* One row's 128 columns to 16 lanes: the sum over the parts in ascending order (of
  * both planes where there are two), the activation, and rows or codes. */
 __global__ __launch_bounds__(256) void block_finish_kernel(BlockGemmParams p)
@@ -927,66 +1148,152 @@ __global__ __launch_bounds__(256) void block_finish_kernel(BlockGemmParams p)
 
 namespace {
 
-/* Tiles: tokens, rows of w, K blocks in the ring, workgroups a compute unit. */
+/* Forms of the kernels: tokens and rows of w a workgroup, workgroups that run at once
+ * on a compute unit; and the time of one, in us: `begin` and, for each K block, `full`
+ * where the device is full of them and `least` where it is not (with `exact` times
+ * that for rows of fp32).  Fitted to timed calls of every form with 1 to 16 parts of K
+ * over 138 sizes (one to 4096 tokens, 128 to 16384 columns, K of 1000 to 8192; a
+ * matrix or two; bf16, codes, fp32): the form that the times choose takes 1.02 of
+ * the best form's time in geometric mean.  us of one form and of the next best:
+ *   1 x 8192x8192       rows of 16 with 8 wavefronts 16.1, with 4 (two workgroups a
+ *                       unit) 16.9;  1 x 16384x8192  28.7, 28.6;  1 x 12000x2048
+ *                       9.7, 7.8
+ *   24 x 8192x8192      rows of 32 17.3, of 64 18.8;  48 x 8192x8192  28.7, 20.2
+ *   200 x 4096x4096     stream 12.1, rows of 64 16.3, tiles 128 x 64 16.5
+ *   128 x 16384x8192    tiles 128 x 64 38.7, stream 49.9;  100 x 8192x8192  two parts
+ *                       24.6, 24.2
+ *   512 x 8192x8192     tiles 128 x 128 45.9, 128 x 64 59.1, of two workgroups a unit
+ *                       59.3 (two parts 54.5)
+ *   2048 x 4096x4096    two workgroups a unit 41.9, one 46.4, tiles 256 x 256 48.5
+ *   4096 x 4096x4096    tiles 256 x 256 67.4, 128 x 128 79.1 */
+enum { ROWS16, ROWS16_PAIR, ROWS32, ROWS64, STREAM, TILE_64, TILE_128, TILE_128_PAIR, TILE_256, FORMS };
 struct Form {
-    int32_t tx, tw, st, resident;
+    int32_t tx, tw, resident;
+    double begin, least, full, exact;
 };
-constexpr Form kForms[] = {{16, 32, 3, 1}, {64, 32, 3, 1}, {128, 128, 2, 2}, {256, 256, 2, 1}, {128, 128, 4, 1}, {128, 64, 6, 1}, {128, 32, 6, 1}, {64, 128, 6, 1}, {128, 128, 4, 1}};
+constexpr Form kForms[FORMS] = {
+    {16, 32, 1, 1.8, 0.06, 0.12, 1.3},    {16, 32, 2, 0.85, 0.08, 0.24, 1.4},  {32, 32, 1, 1.9, 0.08, 0.145, 1.3},
+    {64, 32, 1, 1.7, 0.13, 0.20, 1.35},   {128, 32, 1, 2.1, 0.19, 0.27, 1.5},  {128, 64, 1, 2.8, 0.33, 0.38, 1.8},
+    {128, 128, 1, 3.6, 0.45, 0.59, 1.9},  {128, 128, 2, 3.1, 0.69, 1.14, 1.6}, {256, 256, 1, 6.7, 1.25, 1.68, 0.0}};
+
+/* fp32 planes of [M][ldp] that a part of K leaves: a scale of codes needs 128 columns
+ * in one workgroup. */
+int32_t planes_of(const BlockGemmParams &p, int32_t form, int32_t splits)
+{
+    return splits > 1 ? 1 + p.two : p.q.codes && form != TILE_256 ? 1 : 0;
+}
+
+int64_t units_of(const BlockGemmParams &p, int32_t form)
+{
+    const int64_t tx = kForms[form].tx, tn = kForms[form].tw >> p.two;
+    return (p.M + tx - 1) / tx * ((p.N + tn - 1) / tn);
+}
+
+double time_of(const BlockGemmParams &p, int32_t form, int32_t splits, int32_t cus)
+{
+    const Form &f = kForms[form];
+    const int64_t units = units_of(p, form) * splits, most = (int64_t)f.resident * cus, rounds = (units + most - 1) / most;
+    const double load = (double)units / (double)(rounds * most);
+    const double block = std::max(f.least, f.full * load) * (p.exact ? f.exact : 1.0);
+    const double tiles = 2.0 + (double)rounds * (f.begin + (double)((p.nk + splits - 1) / splits) * block);
+    /* weights at 5.2 TB/s, x at 20 */
+    const double memory = 2.5 + (1.0 + p.two) * (double)p.N * (double)p.K / 5.2e6 + (double)p.M * (double)p.K / 2e7;
+    const int32_t planes = planes_of(p, form, splits);
+    /* the second kernel, and its planes there and back */
+    const double finish = planes ? 5.0 + 1.4e-6 * planes * splits * (double)p.M * (double)p.N : 0.0;
+    /* the shorter of the two is not all hidden */
+    return std::max(tiles, memory) + 0.1 * std::min(tiles, memory) + finish;
+}
 
 } /* namespace */
 
 int64_t block_plan(BlockGemmParams &p, int32_t splits, int32_t cus)
 {
     p.exact = p.y && p.y_f32;
-    const int32_t force = splits >> 16;     /* TIMING */
-    splits &= 0xFFFF;
-    p.form = force ? force - 1 : p.M <= 16 ? 0 : p.M <= 64 ? 1 : 2;
-    if (p.form == 3 && p.exact) p.form = 2;
-    int64_t units = 1;
-    if (p.form >= 2) {
-        const Form &f = kForms[p.form];
-        const int32_t tn = f.tw >> p.two;
-        units = ((int64_t)p.M + f.tx - 1) / f.tx * (((int64_t)p.N + tn - 1) / tn);
-        p.resident = f.resident * cus;
+    p.form = TILE_128;
+    p.splits = 1;
+    double best = 1e300;
+    for (int32_t form = 0; form < FORMS; ++form) {
+        const int32_t tx = kForms[form].tx;
+        if (form == TILE_256 && p.exact) continue;      /* its registers are full */
+        /* rows and streams are for weights that pass by few tokens (4096 x 256x8192:
+         * stream 40.9 us, tiles 128 x 64 in two parts 22.2) */
+        if (form < STREAM ? p.M > 4 * tx : form == STREAM && p.M > 4 * (int64_t)p.N) continue;
+        /* parts: as told, at most one a K block; else up to 16 of two blocks or more
+         * (of tiles: rows already share K among wavefronts) */
+        const int32_t told = std::max(1, std::min({splits, p.nk, 256}));
+        for (int32_t s = splits ? told : 1; s <= (splits ? told : form < STREAM ? 1 : 16) && (splits || s == 1 || 2 * s <= p.nk); s *= 2) {
+            const double t = time_of(p, form, s, cus);
+            if (t < best) {
+                best = t;
+                p.form = form;
+                p.splits = s;
+            }
+        }
     }
-    p.splits = std::max(1, std::min({splits, p.nk, 256}));
-    /* a scale of codes needs 128 columns in one workgroup */
-    p.part_planes = p.splits > 1 ? 1 + p.two : p.q.codes && p.form != 3 ? 1 : 0;
+    p.resident = kForms[p.form].resident * cus;
+    p.part_planes = planes_of(p, p.form, p.splits);
     p.ldp = ((int64_t)p.N + 3) / 4 * 4;
     p.part = nullptr;
-    return std::max(units * p.splits, (((int64_t)p.M + 15) / 16) * (((int64_t)p.N + 127) / 128));
+    return std::max(units_of(p, p.form) * p.splits, (((int64_t)p.M + 15) / 16) * (((int64_t)p.N + 127) / 128));
 }
 
 namespace {
 
-template <int FX, int NW, int ST>
-void launch_rows(const BlockGemmParams &p, hipStream_t stream)
+/* The workgroups of a form whose grid has one each. */
+dim3 whole_grid(const BlockGemmParams &p, int32_t form)
 {
-    const int64_t cols = p.two ? 16 : 32;
-    const dim3 grid((uint32_t)((p.N + cols - 1) / cols), (uint32_t)((p.M + 16 * FX - 1) / (16 * FX)), (uint32_t)p.splits), block(NW * 64);
-    if (p.two && p.exact)
-        hipLaunchKernelGGL((block_rows_kernel<FX, 2, NW, ST, true, true>), grid, block, 0, stream, p);
-    else if (p.two)
-        hipLaunchKernelGGL((block_rows_kernel<FX, 2, NW, ST, true, false>), grid, block, 0, stream, p);
-    else if (p.exact)
-        hipLaunchKernelGGL((block_rows_kernel<FX, 2, NW, ST, false, true>), grid, block, 0, stream, p);
-    else
-        hipLaunchKernelGGL((block_rows_kernel<FX, 2, NW, ST, false, false>), grid, block, 0, stream, p);
+    const int64_t tx = kForms[form].tx, tn = kForms[form].tw >> p.two;
+    return dim3((uint32_t)((p.N + tn - 1) / tn), (uint32_t)((p.M + tx - 1) / tx), (uint32_t)p.splits);
 }
 
-template <int FORM, int WX, int WW, int MINB, bool EXACT>
+template <int FORM, int NW, int ST>
+void launch_rows(const BlockGemmParams &p, hipStream_t stream)
+{
+    constexpr int FX = kForms[FORM].tx / 16, FW = kForms[FORM].tw / 16;
+    const dim3 grid = whole_grid(p, FORM), block(NW * 64);
+    if (p.two && p.exact)
+        hipLaunchKernelGGL((block_rows_kernel<FX, FW, NW, ST, true, true>), grid, block, 0, stream, p);
+    else if (p.two)
+        hipLaunchKernelGGL((block_rows_kernel<FX, FW, NW, ST, true, false>), grid, block, 0, stream, p);
+    else if (p.exact)
+        hipLaunchKernelGGL((block_rows_kernel<FX, FW, NW, ST, false, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((block_rows_kernel<FX, FW, NW, ST, false, false>), grid, block, 0, stream, p);
+}
+
+void launch_stream(const BlockGemmParams &p, hipStream_t stream)
+{
+    const dim3 grid = whole_grid(p, STREAM), block(448);
+    if (p.two && p.exact)
+        hipLaunchKernelGGL((block_stream_kernel<2, 3, 7, true, true>), grid, block, 0, stream, p);
+    else if (p.two)
+        hipLaunchKernelGGL((block_stream_kernel<2, 3, 7, true, false>), grid, block, 0, stream, p);
+    else if (p.exact)
+        hipLaunchKernelGGL((block_stream_kernel<2, 3, 7, false, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((block_stream_kernel<2, 3, 7, false, false>), grid, block, 0, stream, p);
+}
+
+template <int FORM, int WX, int WW, int ST, int MINB, bool EXACT>
 void launch_tile(const BlockGemmParams &p, hipStream_t stream)
 {
-    constexpr int TX = kForms[FORM].tx, TW = kForms[FORM].tw, ST = kForms[FORM].st;
-    const int64_t tn = p.two ? TW / 2 : TW;
-    const int64_t units = (((int64_t)p.M + TX - 1) / TX) * ((p.N + tn - 1) / tn) * p.splits;
+    constexpr int TX = kForms[FORM].tx, TW = kForms[FORM].tw;
+    const int64_t tn = TW >> p.two, units = (((int64_t)p.M + TX - 1) / TX) * ((p.N + tn - 1) / tn) * p.splits;
     const dim3 grid((uint32_t)std::min<int64_t>(units, p.resident)), block(WX * WW * 64);
-    if constexpr (TW > 32)
-        if (p.two) {
-            hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, ST, MINB, true, EXACT>), grid, block, 0, stream, p);
-            return;
-        }
-    hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, ST, MINB, false, EXACT>), grid, block, 0, stream, p);
+    if (p.two)
+        hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, ST, MINB, true, EXACT>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((block_tile_kernel<TX, TW, WX, WW, ST, MINB, false, EXACT>), grid, block, 0, stream, p);
+}
+
+template <int FORM, int WX, int WW, int ST, int MINB>
+void launch_either(const BlockGemmParams &p, hipStream_t stream)
+{
+    if (p.exact)
+        launch_tile<FORM, WX, WW, ST, MINB, true>(p, stream);
+    else
+        launch_tile<FORM, WX, WW, ST, MINB, false>(p, stream);
 }
 
 } /* namespace */
@@ -994,15 +1301,15 @@ void launch_tile(const BlockGemmParams &p, hipStream_t stream)
 hipError_t launch_block_gemm(const BlockGemmParams &p, hipStream_t stream)
 {
     switch (p.form) {
-    case 0: launch_rows<1, 8, 3>(p, stream); break;
-    case 1: launch_rows<4, 4, 3>(p, stream); break;
-    case 2: p.exact ? launch_tile<2, 2, 2, 2, true>(p, stream) : launch_tile<2, 2, 2, 2, false>(p, stream); break;
-    case 3: launch_tile<3, 4, 2, 2, false>(p, stream); break;
-    case 4: p.exact ? launch_tile<4, 2, 2, 1, true>(p, stream) : launch_tile<4, 2, 2, 1, false>(p, stream); break;
-    case 5: p.exact ? launch_tile<5, 2, 2, 1, true>(p, stream) : launch_tile<5, 2, 2, 1, false>(p, stream); break;
-    case 6: p.exact ? launch_tile<6, 2, 1, 1, true>(p, stream) : launch_tile<6, 2, 1, 1, false>(p, stream); break;
-    case 8: p.exact ? launch_tile<8, 2, 4, 2, true>(p, stream) : launch_tile<8, 2, 4, 2, false>(p, stream); break;
-    default: p.exact ? launch_tile<7, 1, 4, 1, true>(p, stream) : launch_tile<7, 1, 4, 1, false>(p, stream); break;
+    case ROWS16: launch_rows<ROWS16, 8, 3>(p, stream); break;
+    case ROWS16_PAIR: launch_rows<ROWS16_PAIR, 4, 3>(p, stream); break;
+    case ROWS32: launch_rows<ROWS32, 8, 2>(p, stream); break;
+    case ROWS64: launch_rows<ROWS64, 4, 3>(p, stream); break;
+    case STREAM: launch_stream(p, stream); break;
+    case TILE_64: launch_either<TILE_64, 2, 2, 6, 1>(p, stream); break;
+    case TILE_128: launch_either<TILE_128, 2, 4, 4, 2>(p, stream); break;
+    case TILE_128_PAIR: launch_either<TILE_128_PAIR, 2, 2, 2, 2>(p, stream); break;
+    default: launch_tile<TILE_256, 4, 2, 2, 2, false>(p, stream); break;
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.part_planes) return e;

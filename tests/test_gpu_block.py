@@ -338,6 +338,46 @@ def test_gemm_exact(M, N, K, splits):
     assert np.array_equal(y.cpu().numpy().astype(np.float64), X @ W.T)
 
 
+# sizes that the larger forms are chosen for (of 256 compute units): streams of 128
+# tokens, tiles from 128 x 64 to 256 x 256, whole and in parts of K, one unit a workgroup
+# and several
+LARGE = [(267, 68, 203), (291, 33, 139), (296, 34, 2453), (257, 79, 2722), (274, 35, 406), (131, 8812, 310), (137, 8214, 149),
+         (386, 11371, 131), (925, 10981, 150), (700, 6100, 400), (4200, 1100, 130), (1300, 9000, 260), (2100, 8300, 149)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_gemm_exact_large(M, N, K):
+    """As above, and rows of bf16: the exact sums rounded once; rows behind the last
+    and columns behind a row's stay as they were."""
+    rng = np.random.default_rng(M + N + K)
+    x, X = whole_matrix(rng, M, K, 1, -3, 0, pad=16, spad=1)
+    w, W = whole_matrix(rng, N, K, 128, -3, 1, pad=32, spad=2)
+    ref = dev(X) @ dev(W).T
+    for out in ("f32", "bf16"):
+        for ld, off in ((0, 0), (N + 3, 1), (N + 8 - N % 8, 0)):
+            assert torch.equal(run_gemm(x, w, out, 0, ld, off).double(), ref.to(DT[out]).double()), (out, ld, off)
+
+
+@pytest.mark.parametrize("kind", ("silu", "gelu"))
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_gated_large(M, N, K, kind):
+    """Both sums exact (scales of 2^-9 on x keep them near the activation's bend), so
+    that the activation's rounding alone is left."""
+    rng = np.random.default_rng(M + N + K + 1)
+    x, X = whole_matrix(rng, M, K, 1, -9, -8, pad=16)
+    (gate, G), (up, U) = (whole_matrix(rng, N, K, 128, -3, 1, spad=2) for _ in range(2))
+    gr, ur = ((dev(X) @ dev(B).T).cpu().numpy() for B in (G, U))
+    h = block.act(gr, kind) * ur
+    off_by = (6 * z_of(gr, kind) + 10) * 2.0 ** -23 * np.abs(h) + 2.0 ** -120 * np.abs(gr * ur) + 1e-37
+    for out, ld, off in (("bf16", 0, 0), ("bf16", N + 3, 1), ("f32", N + 8 - N % 8, 0), ("8bit", 0, 0)):
+        y = run_gated(x, gate, up, kind, out, 0, ld, off)
+        if out == "8bit":
+            check_codes(y, h, off_by)
+            continue
+        err = np.abs(y.double().cpu().numpy() - h)
+        assert np.all(err <= off_by + HALF[out] * (np.abs(h) + off_by)), (out, float(err.max()))
+
+
 def test_gemm_nothing_along_k():
     x, w = Matrix(np.zeros((5, 0), np.uint8), np.zeros((5, 0), np.float32), 1), Matrix(np.zeros((70, 0), np.uint8), np.zeros((1, 0), np.float32), 128)
     for out in ("f32", "bf16"):

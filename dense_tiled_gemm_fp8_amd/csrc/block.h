@@ -55,7 +55,7 @@ struct BlockGemmParams {
     int32_t y_f32, vec;           /* vec: rows of y 16-byte aligned          */
     BlockMat q;
     /* the plan (block_plan) */
-    int32_t exact;                /* 1: products in bf16, summed in fp32     */
+    int32_t exact;                /* 1: products exact, every sum of 32 bits */
     int32_t form;                 /* kernel: index of its table              */
     int32_t resident;             /* workgroups that run at once             */
     int32_t splits;               /* parts of K; more than one, or rows that

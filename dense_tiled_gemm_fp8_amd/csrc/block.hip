@@ -14,10 +14,11 @@
  * The 8-bit instruction sums products in groups of 8 K-values, each product cut
  * off at 2^-13 of the largest of its group (measured: 1 + 2^-13 within a group of
  * 8 is exact, 1 + 2^-14 is 1, and between groups 24 bits are kept).  Against normal
- * data that is 2e-4 of the result's size: a ninth of bf16's rounding, which it is
- * used for, and of 8-bit codes'.  Rows of fp32 are promised sums of 32 bits: for
- * them (EXACT) the codes become bf16, which holds them exactly, and the 16-bit
- * instruction sums them in fp32 at half the rate.
+ * data that is 3e-4 of the result's size: a sixth of bf16's rounding, which it is
+ * used for.  Rows of fp32, and codes whose scales are fp32, are made from sums of 32
+ * bits: for them (EXACT) the codes of x and w become bf16, which holds them exactly,
+ * and the 16-bit instruction sums them in fp32 at half the rate (4096 x 4096x4096:
+ * rows of bf16 67 us, of fp32 126).
  *
  *   block_rows_kernel    few tokens: the stream of weights counts
  *   block_tile_kernel    many tokens: the matrix units count
@@ -407,8 +408,9 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
     constexpr int OF = OC < 32 ? 1 : OC / 32, QUADS = OC < 32 ? 2 : 4;
     constexpr bool EARLY = FW > 2;                 /* tokens' copies in row 1 */
     constexpr bool HALVES = TWO && FW == 1;        /* both matrices in one matrix block */
+    constexpr bool BY_WAVE = TWO && NW * 8 % WTW == 0;      /* a wavefront copies one of them */
     static_assert(FX == 2 && NW % 2 == 0 && WTW <= 128 && (ST - 1) * LOADS < 64 && (!EARLY || ST == 2), "tile");
-    static_assert(!TWO || OC % (NW * 8) == 0 || (HALVES && NW * 8 % WTW == 0), "a copy is of one matrix");
+    static_assert(!TWO || OC % (NW * 8) == 0 || BY_WAVE, "a copy is of one matrix");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[ST * STAGE + (TWO && TN == 128 ? WW * TX * 4 : 0)];
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -451,7 +453,7 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
         rx = rsrc_words(p.x + (int64_t)m0 * p.ldx);
         rw = rsrc_words(p.w + (int64_t)n0 * p.ldw);
         if constexpr (TWO) ru = rsrc_words(p.up + (int64_t)n0 * p.ldu);
-        const bool second = HALVES && wave * 8 % WTW >= OC;       /* this wavefront copies up */
+        const bool second = BY_WAVE && wave * 8 % WTW >= OC;       /* this wavefront copies up */
         if (second) rw = ru;
 #pragma unroll
         for (int d = 0; d < XL; ++d) {
@@ -462,7 +464,7 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
         for (int d = 0; d < WL; ++d) {
             int r = (d * NW + wave) * 8 + drow;
             if constexpr (TWO) r = r / WTW * OC + r % OC;
-            const bool u = HALVES ? second : TWO && (d * NW * 8 / OC) % 2 == 1;
+            const bool u = BY_WAVE ? second : TWO && (d * NW * 8 / OC) % 2 == 1;
             woff[d] = n0 + r < p.N ? (uint32_t)(r * (int32_t)(u ? p.ldu : p.ldw) + unit * 16) : kOOB;
         }
         /* rows past the last repeat its scale */
@@ -486,7 +488,7 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
         if constexpr (d < XL) {
             dma16<d * NW * 1024>(rx, base + so + wave * 1024, kb < have ? xoff[d] + k : kOOB);
         } else if constexpr (d < XL + WL) {
-            dma16<XB + (d - XL) * NW * 1024>(TWO && !HALVES && ((d - XL) * NW * 8 / OC) % 2 == 1 ? ru : rw, base + so + wave * 1024,
+            dma16<XB + (d - XL) * NW * 1024>(TWO && !BY_WAVE && ((d - XL) * NW * 8 / OC) % 2 == 1 ? ru : rw, base + so + wave * 1024,
                                              kb < have ? woff[d - XL] + k : kOOB);
         } else {
             constexpr int i = d - XL - WL;
@@ -1165,8 +1167,10 @@ namespace {
  *   512 x 8192x8192     tiles 128 x 128 45.9, 128 x 64 59.1, of two workgroups a unit
  *                       59.3 (two parts 54.5)
  *   2048 x 4096x4096    two workgroups a unit 41.9, one 46.4, tiles 256 x 256 48.5
- *   4096 x 4096x4096    tiles 256 x 256 67.4, 128 x 128 79.1 */
-enum { ROWS16, ROWS16_PAIR, ROWS32, ROWS64, STREAM, TILE_64, TILE_128, TILE_128_PAIR, TILE_256, FORMS };
+ *   4096 x 4096x4096    tiles 256 x 256 66.9, 128 x 256 75.9;  1024 x 8192x8192  87.4,
+ *                       73.4;  into codes, two of 4096x4096  tiles 128 x 256 240, 128 x
+ *                       128 269 */
+enum { ROWS16, ROWS16_PAIR, ROWS32, ROWS64, STREAM, TILE_64, TILE_128, TILE_128_PAIR, TILE_256, TILE_WIDE, FORMS };
 struct Form {
     int32_t tx, tw, resident;
     double begin, least, full, exact;
@@ -1174,13 +1178,14 @@ struct Form {
 constexpr Form kForms[FORMS] = {
     {16, 32, 1, 1.8, 0.06, 0.12, 1.3},    {16, 32, 2, 0.85, 0.08, 0.24, 1.4},  {32, 32, 1, 1.9, 0.08, 0.145, 1.3},
     {64, 32, 1, 1.7, 0.13, 0.20, 1.35},   {128, 32, 1, 2.1, 0.19, 0.27, 1.5},  {128, 64, 1, 2.8, 0.33, 0.38, 1.8},
-    {128, 128, 1, 3.6, 0.45, 0.59, 1.9},  {128, 128, 2, 3.1, 0.69, 1.14, 1.6}, {256, 256, 1, 6.7, 1.25, 1.68, 0.0}};
+    {128, 128, 1, 3.6, 0.45, 0.59, 1.9},  {128, 128, 2, 3.1, 0.69, 1.14, 1.6}, {256, 256, 1, 6.7, 1.25, 1.68, 0.0},
+    {128, 256, 1, 2.2, 1.05, 1.08, 1.7}};
 
 /* fp32 planes of [M][ldp] that a part of K leaves: a scale of codes needs 128 columns
  * in one workgroup. */
 int32_t planes_of(const BlockGemmParams &p, int32_t form, int32_t splits)
 {
-    return splits > 1 ? 1 + p.two : p.q.codes && form != TILE_256 ? 1 : 0;
+    return splits > 1 ? 1 + p.two : p.q.codes && form < TILE_256 ? 1 : 0;
 }
 
 int64_t units_of(const BlockGemmParams &p, int32_t form)
@@ -1209,7 +1214,7 @@ double time_of(const BlockGemmParams &p, int32_t form, int32_t splits, int32_t c
 
 int64_t block_plan(BlockGemmParams &p, int32_t splits, int32_t cus)
 {
-    p.exact = p.y && p.y_f32;
+    p.exact = p.q.codes || p.y_f32;
     p.form = TILE_128;
     p.splits = 1;
     double best = 1e300;
@@ -1309,7 +1314,8 @@ hipError_t launch_block_gemm(const BlockGemmParams &p, hipStream_t stream)
     case TILE_64: launch_either<TILE_64, 2, 2, 6, 1>(p, stream); break;
     case TILE_128: launch_either<TILE_128, 2, 4, 4, 2>(p, stream); break;
     case TILE_128_PAIR: launch_either<TILE_128_PAIR, 2, 2, 2, 2>(p, stream); break;
-    default: launch_tile<TILE_256, 4, 2, 2, 2, false>(p, stream); break;
+    case TILE_256: launch_tile<TILE_256, 4, 2, 2, 2, false>(p, stream); break;
+    default: launch_either<TILE_WIDE, 2, 4, 3, 2>(p, stream); break;
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.part_planes) return e;

@@ -772,15 +772,18 @@ bool capturing(void *stream)
 
 /* ---- block-scaled operators: argument checks ---- */
 
+/* 256 rows of a tile stay within the 32-bit offsets of its copies */
+const int64_t kMaxRow = (int64_t)1 << 22;
+
 gemm355_status check_block(const gemm355_block_matrix &q, BlockMat &b)
 {
     if (q.rows < 0 || q.K < 0 || (q.block_rows != 1 && q.block_rows != 128)) return GEMM355_EINVAL;
-    if (q.rows > ((int64_t)1 << 26) || q.K > kMaxWide) return GEMM355_EUNSUPPORTED;
+    if (q.rows > ((int64_t)1 << 26) || q.K > kMaxRow) return GEMM355_EUNSUPPORTED;
     const int64_t nk = (q.K + 127) / 128, least = q.block_rows == 1 ? q.rows : nk;
     b.ld = q.ld ? q.ld : (q.K + 15) / 16 * 16;
     b.lds = q.ld_scale ? q.ld_scale : least;
     if (b.ld < q.K || b.ld % 16 != 0 || b.lds < least) return GEMM355_EINVAL;
-    if (b.ld > kMaxWide || b.lds > kMaxDim) return GEMM355_EUNSUPPORTED;
+    if (b.ld > kMaxRow || b.lds > kMaxDim) return GEMM355_EUNSUPPORTED;
     if (q.rows > 0 && q.K > 0 && (!q.codes || !q.scales)) return GEMM355_EINVAL;
     if (!aligned(q.codes, 16) || !aligned(q.scales, 4)) return GEMM355_EALIGN;
     b.codes = q.codes;

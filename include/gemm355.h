@@ -766,7 +766,7 @@ GEMM355_API gemm355_status gemm355_attention_workspace(const gemm355_attention_a
  * scales[(r / 128) * ld_scale + b].  The last block of either axis may be short. */
 typedef struct gemm355_block_matrix {
     int64_t rows, K;        /* any sizes >= 0; EUNSUPPORTED: rows above 2^26, K or
-                               ld above 2^23, ld_scale above 2^30             */
+                               ld above 2^22, ld_scale above 2^30             */
     uint8_t *codes;         /* device, row r at codes + r * ld, 16-byte aligned
                                (EALIGN); a row takes K rounded up to 16 bytes, of
                                which those past K are not written and do not

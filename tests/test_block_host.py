@@ -49,8 +49,8 @@ MATRIX = [
     (dict(ld=496), g.EINVAL), (dict(ld=500), g.EINVAL), (dict(ld=520), g.EINVAL), (dict(ld=-512), g.EINVAL),
     (dict(codes=None), g.EINVAL), (dict(scales=None), g.EINVAL),
     (dict(codes=A + 8), g.EALIGN), (dict(scales=A + STEP + 2), g.EALIGN),
-    (dict(rows=(1 << 26) + 1), g.EUNSUPPORTED), (dict(K=(1 << 23) + 1), g.EUNSUPPORTED),
-    (dict(ld=(1 << 23) + 16), g.EUNSUPPORTED), (dict(ld_scale=(1 << 30) + 1), g.EUNSUPPORTED),
+    (dict(rows=(1 << 26) + 1), g.EUNSUPPORTED), (dict(K=(1 << 22) + 1), g.EUNSUPPORTED),
+    (dict(ld=(1 << 22) + 16), g.EUNSUPPORTED), (dict(ld_scale=(1 << 30) + 1), g.EUNSUPPORTED),
 ]
 
 
@@ -182,6 +182,48 @@ def test_scratch_limit():
         assert status(g.gemm355_block_gemm, gemm(splits=4)) in (g.ENOMEM, g.EHIP)    # EHIP: no device to ask
     finally:
         g.gemm355_set_scratch_limit(old)
+
+
+def test_limits_of_the_header():
+    """Both sides of the limits, by the scratch query where they are allowed."""
+    far = A + (1 << 45)
+    wide = dict(K=1 << 22, ld=1 << 22)
+    w = g.make_block_matrix(128, 1 << 22, A + (1 << 46), A + (1 << 47), block_rows=128)
+    assert g.gemm355_block_gemm_workspace(g.make_block_gemm_args(matrix(**wide), w, y=far)) >= 0
+    tall = matrix(rows=1 << 21, K=128, scales=A + (1 << 42))
+    small = g.make_block_matrix(64, 128, A + (1 << 46), A + (1 << 47), block_rows=128)
+    assert g.gemm355_block_gemm_workspace(g.make_block_gemm_args(tall, small, y=far)) == 0
+    # 2^21 rows by 2^26 columns: more workgroups than a launch has
+    many = g.make_block_matrix(1 << 26, 128, A + (1 << 46), A + (1 << 47), block_rows=128)
+    with pytest.raises(g.Gemm355Error) as e:
+        g.gemm355_block_gemm_workspace(g.make_block_gemm_args(tall, many, y=A + (1 << 52)))
+    assert e.value.status == g.EUNSUPPORTED
+    # parts of more than 2^40 bytes
+    some = g.make_block_matrix(1 << 17, 4096, A + (1 << 46), A + (1 << 47), block_rows=128)
+    x = matrix(rows=1 << 17, K=4096, scales=A + (1 << 42))
+    assert g.gemm355_block_gemm_workspace(g.make_block_gemm_args(x, some, y=A + (1 << 52), splits=16)) == 1 << 40
+    with pytest.raises(g.Gemm355Error) as e:
+        g.gemm355_block_gemm_workspace(g.make_block_gemm_args(x, some, y=A + (1 << 52), splits=17))
+    assert e.value.status == g.EUNSUPPORTED
+
+
+def test_kernels_hold_their_sums_in_registers():
+    """Matrix instructions of both kinds, no spills, no accumulation registers (the
+    sums go through vector instructions) in any product kernel; no spills in the
+    norm's."""
+    import re
+    from dense_tiled_gemm_fp8_amd import build
+    for src, least in (("block.hip", 40), ("norm.hip", 8)):
+        bodies = [b for b in re.split(r"\n(?=_ZN4g355\w+:)", open(build.device_asm(src)).read()) if b.startswith("_ZN4g355")]
+        assert len(bodies) >= least
+        for b in bodies:
+            name = b.split(":")[0]
+            assert re.search(r"; ScratchSize: 0\b", b), name
+            if "finish" in name or src == "norm.hip":
+                continue
+            assert re.search(r"; NumAgprs: 0\b", b), name
+            exact = name.split("EEEv")[0].endswith("1")
+            assert ("v_mfma_f32_" in b) and (("_bf16 " in b) if exact else ("f8f6f4" in b)), name
 
 
 def test_struct_layout_matches_header(tmp_path):

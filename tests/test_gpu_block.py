@@ -384,20 +384,22 @@ def test_gemm_nothing_along_k():
         assert not bool(run_gemm(x, w, out).any())
 
 
-def test_gemm_nan_scales_stay_where_they_are():
+@pytest.mark.parametrize("out", ("bf16", "f32"))
+@pytest.mark.parametrize("M,N,K", [(3, 400, 700), (30, 400, 700), (60, 400, 700), (200, 400, 700), (300, 700, 515), (137, 8214, 149),
+                                   (131, 8812, 310), (1300, 9000, 260)])
+def test_gemm_nan_scales_stay_where_they_are(M, N, K, out):
     """A NaN scale of x reaches its row, one of w its 128 columns, a NaN code its
     row or column, and nothing else changes a bit."""
     rng = np.random.default_rng(9)
-    for M, N, K in ((3, 400, 700), (40, 400, 700), (200, 400, 700), (300, 700, 515)):
-        xc, wc = random_codes(rng, M, K), random_codes(rng, N, K)
-        xs, ws = np.ones((M, -(-K // 128)), np.float32), np.ones((-(-N // 128), -(-K // 128)), np.float32)
-        clean = run_gemm(Matrix(xc, xs, 1), Matrix(wc, ws, 128), "f32").cpu().numpy()
-        xs[1, 2], ws[1, 3], xc[2, 600 % K], wc[5, 9] = np.nan, np.nan, 0x7F, 0xFF
-        y = run_gemm(Matrix(xc, xs, 1), Matrix(wc, ws, 128), "f32").cpu().numpy()
-        bad = np.zeros((M, N), bool)
-        bad[1], bad[2], bad[:, 128:256], bad[:, 5] = True, True, True, True
-        assert np.array_equal(np.isnan(y), bad)
-        assert np.array_equal(y[~bad], clean[~bad])
+    xc, wc = random_codes(rng, M, K), random_codes(rng, N, K)
+    xs, ws = np.ones((M, -(-K // 128)), np.float32), np.ones((-(-N // 128), -(-K // 128)), np.float32)
+    clean = run_gemm(Matrix(xc, xs, 1), Matrix(wc, ws, 128), out).float().cpu().numpy()
+    xs[1, 1], ws[1, 0], xc[2, 600 % K], wc[5, 9] = np.nan, np.nan, 0x7F, 0xFF
+    y = run_gemm(Matrix(xc, xs, 1), Matrix(wc, ws, 128), out).float().cpu().numpy()
+    bad = np.zeros((M, N), bool)
+    bad[1], bad[2], bad[:, 128:256], bad[:, 5] = True, True, True, True
+    assert np.array_equal(np.isnan(y), bad)
+    assert np.array_equal(y[~bad], clean[~bad])
 
 
 def z_of(gate, kind):

@@ -1153,33 +1153,37 @@ namespace {
 /* Forms of the kernels: tokens and rows of w a workgroup, workgroups that run at once
  * on a compute unit; and the time of one, in us: `begin` and, for each K block, `full`
  * where the device is full of them and `least` where it is not (with `exact` times
- * that for rows of fp32).  Fitted to timed calls of every form with 1 to 16 parts of K
- * over 138 sizes (one to 4096 tokens, 128 to 16384 columns, K of 1000 to 8192; a
- * matrix or two; bf16, codes, fp32): the form that the times choose takes 1.02 of
+ * that for exact sums).  Fitted to timed calls of every form with 1 to 16 parts of K
+ * over 162 sizes (one to 4096 tokens, 128 to 16384 columns, K of 500 to 8192; a
+ * matrix or two; bf16, codes, fp32): the form that the times choose takes 1.016 of
  * the best form's time in geometric mean.  us of one form and of the next best:
  *   1 x 8192x8192       rows of 16 with 8 wavefronts 16.1, with 4 (two workgroups a
  *                       unit) 16.9;  1 x 16384x8192  28.7, 28.6;  1 x 12000x2048
  *                       9.7, 7.8
  *   24 x 8192x8192      rows of 32 17.3, of 64 18.8;  48 x 8192x8192  28.7, 20.2
+ *   64 x 12000x2048     rows of 64 12.6, two workgroups a unit 9.6;  64 x 2048x8192
+ *                       11.7, 18.4;  rows of 32 with 8 wavefronts and one
+ *                       workgroup a unit are no faster than with 4 and two (24 x
+ *                       8192x8192 17.4, 17.5;  24 x 10000x4096  16.8, 15.1)
  *   200 x 4096x4096     stream 12.1, rows of 64 16.3, tiles 128 x 64 16.5
- *   128 x 16384x8192    tiles 128 x 64 38.7, stream 49.9;  100 x 8192x8192  two parts
- *                       24.6, 24.2
+ *   128 x 16384x8192    tiles 128 x 64 38.7, stream 49.9;  100 x 8192x8192  in two
+ *                       parts 24.6, 24.2
  *   512 x 8192x8192     tiles 128 x 128 45.9, 128 x 64 59.1, of two workgroups a unit
  *                       59.3 (two parts 54.5)
  *   2048 x 4096x4096    two workgroups a unit 41.9, one 46.4, tiles 256 x 256 48.5
  *   4096 x 4096x4096    tiles 256 x 256 66.9, 128 x 256 75.9;  1024 x 8192x8192  87.4,
  *                       73.4;  into codes, two of 4096x4096  tiles 128 x 256 240, 128 x
  *                       128 269 */
-enum { ROWS16, ROWS16_PAIR, ROWS32, ROWS64, STREAM, TILE_64, TILE_128, TILE_128_PAIR, TILE_256, TILE_WIDE, FORMS };
+enum { ROWS16, ROWS16_PAIR, ROWS32, ROWS64, ROWS64_PAIR, STREAM, TILE_64, TILE_128, TILE_128_PAIR, TILE_256, TILE_WIDE, FORMS };
 struct Form {
     int32_t tx, tw, resident;
     double begin, least, full, exact;
 };
 constexpr Form kForms[FORMS] = {
-    {16, 32, 1, 1.8, 0.06, 0.12, 1.3},    {16, 32, 2, 0.85, 0.08, 0.24, 1.4},  {32, 32, 1, 1.9, 0.08, 0.145, 1.3},
-    {64, 32, 1, 1.7, 0.13, 0.20, 1.35},   {128, 32, 1, 2.1, 0.19, 0.27, 1.5},  {128, 64, 1, 2.8, 0.33, 0.38, 1.8},
-    {128, 128, 1, 3.6, 0.45, 0.59, 1.9},  {128, 128, 2, 3.1, 0.69, 1.14, 1.6}, {256, 256, 1, 6.7, 1.25, 1.68, 0.0},
-    {128, 256, 1, 2.2, 1.05, 1.08, 1.7}};
+    {16, 32, 1, 1.5, 0.068, 0.13, 1.0},  {16, 32, 2, 0.62, 0.094, 0.29, 1.0}, {32, 32, 2, 1.3, 0.093, 0.30, 1.0},
+    {64, 32, 1, 2.5, 0.14, 0.19, 1.1},   {64, 32, 2, 2.4, 0.23, 0.28, 1.4},    {128, 32, 1, 2.0, 0.21, 0.25, 1.4},
+    {128, 64, 1, 3.1, 0.34, 0.34, 1.8},  {128, 128, 1, 3.8, 0.44, 0.54, 1.9},  {128, 128, 2, 4.0, 0.65, 1.1, 1.6},
+    {256, 256, 1, 6.6, 1.2, 1.6, 0.0},   {128, 256, 1, 5.3, 0.80, 0.95, 1.7}};
 
 /* fp32 planes of [M][ldp] that a part of K leaves: a scale of codes needs 128 columns
  * in one workgroup. */
@@ -1308,8 +1312,9 @@ hipError_t launch_block_gemm(const BlockGemmParams &p, hipStream_t stream)
     switch (p.form) {
     case ROWS16: launch_rows<ROWS16, 8, 3>(p, stream); break;
     case ROWS16_PAIR: launch_rows<ROWS16_PAIR, 4, 3>(p, stream); break;
-    case ROWS32: launch_rows<ROWS32, 8, 2>(p, stream); break;
+    case ROWS32: launch_rows<ROWS32, 4, 2>(p, stream); break;
     case ROWS64: launch_rows<ROWS64, 4, 3>(p, stream); break;
+    case ROWS64_PAIR: launch_rows<ROWS64_PAIR, 2, 3>(p, stream); break;
     case STREAM: launch_stream(p, stream); break;
     case TILE_64: launch_either<TILE_64, 2, 2, 6, 1>(p, stream); break;
     case TILE_128: launch_either<TILE_128, 2, 4, 4, 2>(p, stream); break;

@@ -73,7 +73,9 @@ def rmsnorm(h: np.ndarray, weight: Optional[np.ndarray], eps: float) -> np.ndarr
 
 
 def act(g: np.ndarray, kind: str) -> np.ndarray:
+    """g / (1 + exp(-z)): z = g for SiLU; (1 + tanh(z / 2)) / 2 is the same quotient,
+    without the difference that far below zero loses every digit."""
     g = np.asarray(g, dtype=np.float64)
-    if kind == "silu":
-        return np.where(g >= 0, g / (1 + np.exp(-np.abs(g))), g * np.exp(-np.abs(g)) / (1 + np.exp(-np.abs(g))))
-    return 0.5 * g * (1 + np.tanh(np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)))
+    z = g if kind == "silu" else 2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, g / (1 + e), g * e / (1 + e))

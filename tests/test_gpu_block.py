@@ -329,8 +329,8 @@ def whole_matrix(rng, rows, K, block_rows, low, high, **kw):
 @pytest.mark.parametrize("M,N,K", [(1, 300, 2000), (7, 513, 1111), (16, 256, 4096), (40, 400, 1024), (64, 384, 2050), (128, 700, 1300),
                                    (200, 512, 640), (257, 385, 1024), (600, 1030, 515)])
 def test_gemm_exact(M, N, K, splits):
-    """Products of at most 16 * 2, sums of at most 2^5 K <= 2^17, in steps of 2^-6:
-    23 bits, exact whatever the order."""
+    """Products of at most 16 * 2, sums of at most 2^5 K <= 2^17.5, in steps of 2^-6:
+    under 2^24 of them, exact whatever the order."""
     rng = np.random.default_rng(M + N + K + splits)
     x, X = whole_matrix(rng, M, K, 1, -3, 0, pad=16)
     w, W = whole_matrix(rng, N, K, 128, -3, 1)
@@ -338,11 +338,14 @@ def test_gemm_exact(M, N, K, splits):
     assert np.array_equal(y.cpu().numpy().astype(np.float64), X @ W.T)
 
 
-# sizes that the larger forms are chosen for (of 256 compute units): streams of 128
-# tokens, tiles from 128 x 64 to 256 x 256, whole and in parts of K, one unit a workgroup
-# and several
-LARGE = [(267, 68, 203), (291, 33, 139), (296, 34, 2453), (257, 79, 2722), (274, 35, 406), (131, 8812, 310), (137, 8214, 149),
-         (386, 11371, 131), (925, 10981, 150), (700, 6100, 400), (4200, 1100, 130), (1300, 9000, 260), (2100, 8300, 149)]
+# sizes that each form is chosen for (of 256 compute units) with one matrix and with
+# two, for bf16, codes and fp32: rows of 16, 32 and 64 tokens, streams of 128, tiles from
+# 128 x 64 to 256 x 256, whole and in parts of K, one unit a workgroup and several
+LARGE = [(1, 33, 4329), (1, 533, 4294), (66, 35, 138), (153, 34, 133), (129, 36, 145), (259, 33, 131), (267, 68, 203),
+         (291, 33, 139), (296, 34, 2453), (257, 79, 2722), (274, 35, 406), (52, 4097, 268), (33, 5655, 142), (49, 8582, 139),
+         (36, 12398, 130), (131, 8812, 310), (137, 8214, 149), (286, 11320, 129), (386, 11371, 131), (925, 10981, 150),
+         (700, 6100, 400), (257, 9972, 1229), (2053, 33, 3795), (2101, 33, 5166), (2134, 70, 5722), (1028, 6068, 1301),
+         (1319, 5909, 133), (4200, 1100, 130), (1300, 9000, 260), (2100, 8300, 149)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)

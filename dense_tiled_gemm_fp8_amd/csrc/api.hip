@@ -816,7 +816,6 @@ struct Rows {
     {
     }
     bool same(const Rows &o) const { return ptr == o.ptr && ld == o.ld && es == o.es; }
-    bool vec() const { return aligned(ptr, 16) && ld * es % 16 == 0; }
 };
 
 gemm355_status norm_setup(const gemm355_rmsnorm_args *a, NormParams &p)
@@ -868,7 +867,6 @@ gemm355_status norm_setup(const gemm355_rmsnorm_args *a, NormParams &p)
     p.r_f32 = r.es == 4;
     p.w_f32 = a->w_type == GEMM355_SRC_F32;
     p.y_f32 = y.es == 4;
-    p.vec = x.vec() && (!a->residual || r.vec()) && (!a->sum || h.vec()) && (!a->y || y.vec()) && aligned(a->weight, 16);
     p.eps = a->eps;
     return GEMM355_OK;
 }
@@ -948,7 +946,6 @@ gemm355_status block_setup(const BlockCall &c, BlockGemmParams &p, size_t &bytes
     p.y = c.y;
     p.ldy = y.ld;
     p.y_f32 = y.es == 4;
-    p.vec = y.vec();
     const int64_t groups = block_plan(p, c.splits, present_cus());
     if (groups > kMaxBlocks) return GEMM355_EUNSUPPORTED;
     const double need = (double)p.part_planes * p.splits * (double)M * (double)p.ldp * 4.0;
@@ -1026,7 +1023,6 @@ gemm355_status gemm355_block_quantize(const void *x, int64_t ld, gemm355_src src
     p.rows = (int32_t)q->rows;
     p.K = (int32_t)q->K;
     p.f32 = rows.es == 4;
-    p.vec = rows.vec();
     p.block_rows = q->block_rows;
     return launch_block_quantize(p, (hipStream_t)stream) == hipSuccess ? GEMM355_OK : GEMM355_EHIP;
 }

@@ -26,7 +26,6 @@ struct BlockQuantParams {
     int64_t ldx;                  /* elements                                */
     int32_t rows, K;
     int32_t f32;                  /* x: 1 fp32, 0 bf16                       */
-    int32_t vec;                  /* rows of x 16-byte aligned               */
     int32_t block_rows;           /* 1 or 128                                */
 };
 
@@ -37,7 +36,6 @@ struct NormParams {
     int64_t ldx, ldr, lds, ldy;   /* elements                                */
     int32_t rows, width;
     int32_t x_f32, r_f32, w_f32, y_f32;
-    int32_t vec;                  /* every row 16-byte aligned               */
     float eps;
 };
 
@@ -52,7 +50,7 @@ struct BlockGemmParams {
     int32_t act;                  /* of two: 0 SiLU, 1 GELU (tanh)           */
     void *y;                      /* rows, or null: codes                    */
     int64_t ldy;
-    int32_t y_f32, vec;           /* vec: rows of y 16-byte aligned          */
+    int32_t y_f32;
     BlockMat q;
     /* the plan (block_plan) */
     int32_t exact;                /* 1: products exact, every sum of 32 bits */

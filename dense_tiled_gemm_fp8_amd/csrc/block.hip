@@ -75,16 +75,21 @@ __device__ __forceinline__ float gated(float g, float u, int32_t act)
     return g / (1.0f + __expf(-z)) * u;
 }
 
+/* Memory takes vectors at any address of whole elements. */
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 /* Four sums of consecutive columns from n on, as rows of y. */
 __device__ __forceinline__ void store4(const BlockGemmParams &p, int32_t m, int32_t n, const f32x4 &v)
 {
     const int64_t at = (int64_t)m * p.ldy + n;
     const float a = v[0], b = v[1], c = v[2], d = v[3];
-    if (p.vec && n + 4 <= p.N) {
+    if (n + 4 <= p.N) {
         if (p.y_f32)
-            *(float4 *)((float *)p.y + at) = make_float4(a, b, c, d);
+            *(f32x4_any *)((float *)p.y + at) = f32x4_any{a, b, c, d};
         else
-            *(uint2 *)((uint16_t *)p.y + at) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+            *(u32x2_any *)((uint16_t *)p.y + at) = u32x2_any{pack_bf16(a, b), pack_bf16(c, d)};
         return;
     }
     const float e[4] = {a, b, c, d};
@@ -311,7 +316,7 @@ __device__ __forceinline__ void store_part(const BlockGemmParams &p, float *plan
 template <int QUADS>
 __device__ __forceinline__ void store_rows(const BlockGemmParams &p, const Place &at, const f32x16 &v)
 {
-    if (p.vec && !p.y_f32) {
+    if (!p.y_f32) {
         /* 8 columns a lane: quads 0 and 1 (2 and 3) of both halves trade places */
 #pragma unroll
         for (int q = 0; q < QUADS; q += 2) {
@@ -329,7 +334,7 @@ __device__ __forceinline__ void store_rows(const BlockGemmParams &p, const Place
             if (at.m >= p.M || n >= p.N) continue;
             uint16_t *o = (uint16_t *)p.y + (int64_t)at.m * p.ldy + n;
             if (n + 8 <= p.N) {
-                *(uint4 *)o = make_uint4(d[0][0], d[0][1], d[1][0], d[1][1]);
+                *(u32x4_any *)o = u32x4_any{d[0][0], d[0][1], d[1][0], d[1][1]};
                 continue;
             }
 #pragma unroll
@@ -400,7 +405,7 @@ __device__ __forceinline__ void store_codes(const BlockGemmParams &p, const Plac
 template <int TX, int TW, int WX, int WW, int ST, int MINB, bool TWO, bool EXACT>
 __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemmParams p)
 {
-    constexpr int NW = WX * WW, WTX = TX / WX, WTW = TW / WW, FX = WTX / 32, FW = WTW / 32;
+    constexpr int NW = WX * WW, WTX = TX / WX, WTW = TW / WW, FW = WTW / 32;
     constexpr int XB = TX * 128, WB = TW * 128, SCX = XB + WB, SCW = SCX + TX * 4, STAGE = SCW + 256;
     constexpr int SCG = TX / 64 + 1, SL = (SCG + NW - 1) / NW;       /* scale copies of a stage, of a wavefront */
     constexpr int XL = TX / 8 / NW, WL = TW / 8 / NW, LOADS = XL + WL + SL;
@@ -409,7 +414,7 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
     constexpr bool EARLY = FW > 2;                 /* tokens' copies in row 1 */
     constexpr bool HALVES = TWO && FW == 1;        /* both matrices in one matrix block */
     constexpr bool BY_WAVE = TWO && NW * 8 % WTW == 0;      /* a wavefront copies one of them */
-    static_assert(FX == 2 && NW % 2 == 0 && WTW <= 128 && (ST - 1) * LOADS < 64 && (!EARLY || ST == 2), "tile");
+    static_assert(WTX == 64 && NW % 2 == 0 && WTW <= 128 && (ST - 1) * LOADS < 64 && (!EARLY || ST == 2), "tile");
     static_assert(!TWO || OC % (NW * 8) == 0 || BY_WAVE, "a copy is of one matrix");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[ST * STAGE + (TWO && TN == 128 ? WW * TX * 4 : 0)];
 

@@ -34,28 +34,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 
 __device__ __forceinline__ float as_bf16(float v) { return (float)(__bf16)v; }
 
+/* Memory takes vectors at any address of whole elements. */
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 /* `left` (at most 8) elements from base[at] on; the others are zero. */
-__device__ __forceinline__ void load8(const void *base, int64_t at, int32_t left, bool f32, bool vec, float (&v)[8])
+__device__ __forceinline__ void load8(const void *base, int64_t at, int32_t left, bool f32, float (&v)[8])
 {
-    if (vec && left >= 8) {
+    if (left >= 8) {
         if (f32) {
-            const float4 a = *(const float4 *)((const float *)base + at);
-            const float4 b = *(const float4 *)((const float *)base + at + 4);
-            v[0] = a.x;
-            v[1] = a.y;
-            v[2] = a.z;
-            v[3] = a.w;
-            v[4] = b.x;
-            v[5] = b.y;
-            v[6] = b.z;
-            v[7] = b.w;
-        } else {
-            const uint4 a = *(const uint4 *)((const uint16_t *)base + at);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+            const f32x4_any *x = (const f32x4_any *)((const float *)base + at);
+            const f32x4_any a = x[0], b = x[1];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                v[2 * j] = bf16_value(w[j] & 0xFFFFu);
-                v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+                v[j] = a[j];
+                v[4 + j] = b[j];
+            }
+        } else {
+            const u32x4_any a = *(const u32x4_any *)((const uint16_t *)base + at);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t w = a[j];
+                v[2 * j] = bf16_value(w & 0xFFFFu);
+                v[2 * j + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
             }
         }
         return;
@@ -67,15 +68,16 @@ __device__ __forceinline__ void load8(const void *base, int64_t at, int32_t left
     }
 }
 
-__device__ __forceinline__ void store8(void *base, int64_t at, int32_t left, bool f32, bool vec, const float (&v)[8])
+__device__ __forceinline__ void store8(void *base, int64_t at, int32_t left, bool f32, const float (&v)[8])
 {
-    if (vec && left >= 8) {
+    if (left >= 8) {
         if (f32) {
-            *(float4 *)((float *)base + at) = make_float4(v[0], v[1], v[2], v[3]);
-            *(float4 *)((float *)base + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            f32x4_any *y = (f32x4_any *)((float *)base + at);
+            y[0] = f32x4_any{v[0], v[1], v[2], v[3]};
+            y[1] = f32x4_any{v[4], v[5], v[6], v[7]};
         } else {
-            *(uint4 *)((uint16_t *)base + at) =
-                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+            *(u32x4_any *)((uint16_t *)base + at) =
+                u32x4_any{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
         }
         return;
     }
@@ -122,6 +124,21 @@ __device__ __forceinline__ float max16(float a)
     return fmaxf(a, lane_move<0x140>(a));
 }
 
+/* Sum over a wavefront, the same in every lane: sixteens as above, then the four of
+ * them in order. */
+__device__ __forceinline__ float sum64(float a)
+{
+    a += lane_move<0xB1>(a);
+    a += lane_move<0x4E>(a);
+    a += lane_move<0x141>(a);
+    a += lane_move<0x140>(a);
+    const int v = __builtin_bit_cast(int, a);
+    float s = 0.0f;
+#pragma unroll
+    for (int l = 0; l < 64; l += 16) s += __builtin_bit_cast(float, __builtin_amdgcn_readlane(v, l));
+    return s;
+}
+
 __device__ __forceinline__ float max8(const float (&v)[8], float a)
 {
 #pragma unroll
@@ -149,7 +166,7 @@ __global__ __launch_bounds__(256) void block_quantize_rows_kernel(BlockQuantPara
     const int32_t row = rb * 16 + (threadIdx.x >> 4), k = kb * 128 + (threadIdx.x & 15) * 8;
     const int32_t left = row < p.rows ? p.K - k : 0;
     float v[8];
-    load8(p.x, (int64_t)row * p.ldx + k, left, p.f32 != 0, p.vec != 0, v);
+    load8(p.x, (int64_t)row * p.ldx + k, left, p.f32 != 0, v);
     const Scale s = block_scale(max16(max8(v, 0.0f)));
     if (row >= p.rows) return;
     if ((threadIdx.x & 15) == 0) p.q.scales[(int64_t)kb * p.q.lds + row] = s.scale;
@@ -167,7 +184,7 @@ __global__ __launch_bounds__(256) void block_quantize_square_kernel(BlockQuantPa
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int32_t row = r0 + i * 16;
-        load8(p.x, (int64_t)row * p.ldx + k, row < p.rows ? p.K - k : 0, p.f32 != 0, p.vec != 0, v[i]);
+        load8(p.x, (int64_t)row * p.ldx + k, row < p.rows ? p.K - k : 0, p.f32 != 0, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) a = max8(v[i], a);
@@ -195,14 +212,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(NormParams p
     constexpr int ROWS = T < 256 ? 256 / T : 1;
     __shared__ float red[T < 256 ? 1 : T / 64];
     const int32_t row = blockIdx.x * ROWS + (T < 256 ? threadIdx.x / T : 0), t = threadIdx.x % T;
-    const bool vec = p.vec != 0;
     const int32_t width = row < p.rows ? p.width : 0;
-    float h[NO][8], r[NO][8];
+    float h[NO][8], r[NO][8], w[NO][8];
 #pragma unroll
     for (int i = 0; i < NO; ++i) {
         const int32_t k = (i * T + t) * 8;
-        load8(p.x, row * p.ldx + k, width - k, p.x_f32 != 0, vec, h[i]);
-        if (p.residual) load8(p.residual, row * p.ldr + k, width - k, p.r_f32 != 0, vec, r[i]);
+        load8(p.x, row * p.ldx + k, width - k, p.x_f32 != 0, h[i]);
+        if (p.residual) load8(p.residual, row * p.ldr + k, width - k, p.r_f32 != 0, r[i]);
+        if (p.weight) load8(p.weight, k, width - k, p.w_f32 != 0, w[i]);
     }
     float total = 0.0f;
 #pragma unroll
@@ -221,8 +238,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(NormParams p
         for (int j = 0; j < 8; ++j) part = __builtin_fmaf(h[i][j], h[i][j], part);
         total += part;
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o, 64);
+    total = sum64(total);
     if constexpr (T >= 256) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = total;
         __syncthreads();
@@ -236,12 +252,11 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(NormParams p
         const int32_t k = (i * T + t) * 8, left = width - k;
         /* the 16 lanes of a block stay together for the maximum */
         if ((i * T + (t & ~15)) * 8 >= width) continue;
-        float w[8], y[8];
-        if (p.sum) store8(p.sum, row * p.lds + k, left, p.r_f32 != 0, vec, h[i]);
-        if (p.weight) load8(p.weight, k, left, p.w_f32 != 0, vec, w);
+        float y[8];
+        if (p.sum) store8(p.sum, row * p.lds + k, left, p.r_f32 != 0, h[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = p.weight ? h[i][j] * by * w[j] : h[i][j] * by;
-        if (p.y) store8(p.y, row * p.ldy + k, left, p.y_f32 != 0, vec, y);
+        for (int j = 0; j < 8; ++j) y[j] = p.weight ? h[i][j] * by * w[i][j] : h[i][j] * by;
+        if (p.y) store8(p.y, row * p.ldy + k, left, p.y_f32 != 0, y);
         if (p.q.codes) {
             const Scale s = block_scale(max16(max8(y, 0.0f)));
             if ((t & 15) == 0) p.q.scales[(int64_t)(k >> 7) * p.q.lds + row] = s.scale;

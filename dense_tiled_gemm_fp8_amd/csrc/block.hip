@@ -20,7 +20,9 @@
  * and the 16-bit instruction sums them in fp32 at half the rate (4096 x 4096x4096:
  * rows of bf16 67 us, of fp32 126).
  *
- *   block_rows_kernel    few tokens: the stream of weights counts
+ *   block_rows_kernel    up to 64 tokens: the stream of weights counts, K split among
+ *                        wavefronts
+ *   block_stream_kernel  some 128 tokens: the same, with wavefronts that only copy
  *   block_tile_kernel    many tokens: the matrix units count
  *   block_finish_kernel  joins parts of K, activates, quantises
  */
@@ -114,6 +116,11 @@ __device__ __forceinline__ void store4(const BlockGemmParams &p, int32_t m, int3
  * LDS rows of 128 bytes; a row's 16-byte unit c lies at c ^ (row / 2 % 8), so that
  * the 16 rows of one read take different banks.  A lane of group h reads units 2h
  * and 2h + 1 of both operands: any order of K is right that both share.
+ *
+ * Memory bounds it for a few tokens: one token by 16384 x 8192, 134 MB, in 31.0 us
+ * (4.3 TB/s; a large copy 4.8 to 5.0), by 8192 x 8192 in 14.9, by two of 8192 x 4096
+ * in 13.0 with exact sums.  With 64 tokens the copies of x, 16 KB beside 4 of weights
+ * a K block and wavefront, count as much: 64 x 8192x8192 in 20.8 us.
  */
 template <int FX, int FW, int NW, int ST, bool TWO, bool EXACT>
 __global__ __launch_bounds__(NW * 64) void block_rows_kernel(BlockGemmParams p)
@@ -401,6 +408,16 @@ __device__ __forceinline__ void store_codes(const BlockGemmParams &p, const Plac
  * A workgroup takes every gridDim.x-th unit (a tile's part of K).  The first copies
  * of its next unit land before it stores the sums of this one, from registers, and
  * nothing waits for the stores before the unit's second K block.
+ *
+ * 256 x 256 tiles: 4096 x 8192x8192 in 236 us, 2.33 PFLOP/s.  A K block takes 1.53 us
+ * (2.8 PFLOP/s), of which multiply-adds cost a tenth and copies a seventh (with each
+ * left out, 8192^3 in 425 and 415 us against 486); matrix instructions run in 0.61 of
+ * all cycles at the 1.78 GHz that the power limit leaves.  A tile's begin and stores
+ * take some 8 us more.  Copies of a K block in one burst 479 us (8192^3), in two 459;
+ * the next unit's copies behind the stores 142 us (8192 x 8192x2048), before them 131.
+ * Exact sums (128 x 256): two of 8192 x 4096 by 2048 tokens in 238 us, 1.15 PFLOP/s,
+ * where the widening of codes, half as many instruction cycles as the products',
+ * stands beside them.
  */
 template <int TX, int TW, int WX, int WW, int ST, int MINB, bool TWO, bool EXACT>
 __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemmParams p)
@@ -883,6 +900,13 @@ __global__ __launch_bounds__(WX *WW * 64, MINB) void block_tile_kernel(BlockGemm
  * ring of WS of w.  Four multiply, 32 tokens each.  A step is B K blocks, whose
  * fragments are read while the step before is multiplied; all meet at one barrier a
  * step.
+ *
+ * 128 x 8192x8192: 23.6 us, where the tiles of 128 x 64 take 31.8 and, in two parts,
+ * 25.8; 128 x 4096x4096 11.0 against 15.6.  Without any data (every copy out of
+ * range) it takes 17.8 of 26.6 us with a step of one K block: the chain of barrier,
+ * fragments and products; x, 16 KB a K block from the L2, and the weights' 4 KB from
+ * memory add to it.  A second wavefront for the weights, or four for x, changed
+ * nothing.
  */
 template <int B, int XS, int WS, bool TWO, bool EXACT>
 __global__ __launch_bounds__(448) void block_stream_kernel(BlockGemmParams p)
@@ -1097,7 +1121,9 @@ __global__ __launch_bounds__(448) void block_stream_kernel(BlockGemmParams p)
 }
 
 /* One row's 128 columns to 16 lanes: the sum over the parts in ascending order (of
- * both planes where there are two), the activation, and rows or codes. */
+ * both planes where there are two), the activation, and rows or codes.  A second
+ * kernel costs some 5 us between calls (3.8 of its own where it has little to do), so
+ * parts pay only where tiles are few. */
 __global__ __launch_bounds__(256) void block_finish_kernel(BlockGemmParams p)
 {
     const int32_t nb = (p.N + 127) >> 7, mb = blockIdx.x / nb, kb = blockIdx.x - mb * nb;

@@ -240,6 +240,16 @@ def test_norm_without_residual(y_type, codes):
     norm_check(40, 300, "f32", "bf16", y_type, codes, "f32", residual=False)
 
 
+def test_norm_without_the_sum():
+    """A residual whose sum is not kept."""
+    x, r = (torch.randn(7, 3000, device="cuda").bfloat16() for _ in range(2))
+    h, a, b = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    g.gemm355_rmsnorm(g.make_rmsnorm_args(7, 3000, x=x, residual=r, sum=h, y=a))
+    g.gemm355_rmsnorm(g.make_rmsnorm_args(7, 3000, x=x, residual=r, y=b))
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
 def test_norm_in_place():
     """sum over the residual, y over x; then sum over x."""
     rng = np.random.default_rng(3)
@@ -348,7 +358,7 @@ LARGE = [(1, 33, 4329), (1, 533, 4294), (66, 35, 138), (153, 34, 133), (129, 36,
          (1319, 5909, 133), (4200, 1100, 130), (1300, 9000, 260), (2100, 8300, 149)]
 
 
-@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("M,N,K", LARGE + [(1284, 11057, 145), (257, 10882, 147), (1410, 15694, 131), (569, 11511, 1172)])
 def test_gemm_exact_large(M, N, K):
     """As above, and rows of bf16: the exact sums rounded once; rows behind the last
     and columns behind a row's stay as they were."""
@@ -379,6 +389,68 @@ def test_gated_large(M, N, K, kind):
             continue
         err = np.abs(y.double().cpu().numpy() - h)
         assert np.all(err <= off_by + HALF[out] * (np.abs(h) + off_by)), (out, float(err.max()))
+
+
+@pytest.mark.parametrize("M,N,K,splits", [(385, 10171, 566, 5), (34, 13207, 527, 5), (524, 12721, 2122, 2), (137, 10186, 518, 5),
+                                          (33, 6824, 522, 5), (5, 100, 1000, 200), (200, 300, 1000, 256)])
+def test_parts_told_large(M, N, K, splits):
+    """More units than workgroups run at once, each a part of K; more parts told than
+    there are K blocks."""
+    rng = np.random.default_rng(M + N + K)
+    x, X = whole_matrix(rng, M, K, 1, -3, 0, pad=16)
+    w, W = whole_matrix(rng, N, K, 128, -3, 1)
+    u, U = whole_matrix(rng, N, K, 128, -3, 1)
+    ref, up = dev(X) @ dev(W).T, dev(X) @ dev(U).T
+    assert torch.equal(run_gemm(x, w, "f32", splits).double(), ref)
+    assert torch.equal(run_gemm(x, w, "bf16", splits), ref.bfloat16())
+    q = run_gated(x, w, u, "silu", "8bit", splits)
+    one = run_gated(x, w, u, "silu", "8bit", 1)
+    assert all(np.array_equal(a, b) for a, b in zip(q.host(), one.host()))
+    y = run_gated(x, w, u, "silu", "bf16", splits).double()
+    h = ref * torch.sigmoid(ref) * up
+    off = (6 * ref.abs() + 10) * 2.0 ** -23 * h.abs() + 2.0 ** -120 * (ref * up).abs() + 1e-37
+    assert bool(((y - h).abs() <= off + HALF["bf16"] * (h.abs() + off)).all())
+
+
+def test_past_32_bit_offsets():
+    """A matrix of weights, rows of activations and outputs of more than 2^32 bytes:
+    the last rows and columns, bit for bit."""
+    N, K = 66000, 65536                                   # 4.3e9 codes
+    w = torch.randint(0, 5, (N, K), device="cuda", dtype=torch.uint8)
+    w += 0x38                                             # 1, 1.125 .. 1.5
+    ws = torch.ones(-(-N // 128), K // 128, device="cuda")
+    wm = g.make_block_matrix(N, K, w, ws, block_rows=128)
+    x, X = whole_matrix(np.random.default_rng(1), 3, K, 1, 0, 0)
+    y = torch.zeros(3, N, device="cuda")
+    g.gemm355_block_gemm(g.make_block_gemm_args(x.m, wm, y=y, out=g.SRC_F32))
+    torch.cuda.synchronize()
+    for n0 in (0, 32768, N - 130):
+        part = w[n0:n0 + 130].view(torch.float8_e4m3fn).double()
+        ref = dev(X) @ part.T                             # sums of eighths under 2^19: exact
+        assert torch.equal(y[:, n0:n0 + 130].double(), ref)
+    # the same bytes as activations: 66000 tokens by 40 columns
+    xs = torch.ones(K // 128, N, device="cuda")
+    xm = g.make_block_matrix(N, K, w, xs)
+    v, V = whole_matrix(np.random.default_rng(2), 40, K, 128, 0, 0)
+    out = torch.zeros(N, 40, device="cuda")
+    g.gemm355_block_gemm(g.make_block_gemm_args(xm, v.m, y=out, out=g.SRC_F32))
+    torch.cuda.synchronize()
+    for m0 in (0, 32768, N - 130):
+        part = w[m0:m0 + 130].view(torch.float8_e4m3fn).double()
+        assert torch.equal(out[m0:m0 + 130].double(), part @ dev(V).T)
+    del out, y
+    # quantised out of bf16 rows of 8.7e9 bytes; a norm over rows of as many
+    src = torch.ones(N, K, dtype=torch.bfloat16, device="cuda")
+    src[-1] = 3.0
+    g.gemm355_block_quantize(src, xm)
+    torch.cuda.synchronize()
+    assert bool((w[-2:] == 0x7E).all()) and bool((w[0] == 0x7E).all())
+    assert float(xs[0, 0]) == float(np.float32(1) / np.float32(448)) and float(xs[-1, -1]) == float(np.float32(3) / np.float32(448))
+    rows, width = N * 8, K // 8
+    r = torch.full((rows, width), 2.0, dtype=torch.bfloat16, device="cuda")
+    g.gemm355_rmsnorm(g.make_rmsnorm_args(rows, width, x=src, residual=r, sum=r, y=src))
+    torch.cuda.synchronize()
+    assert bool((r[-1] == 5).all()) and bool((r[0] == 3).all()) and bool((src[-1] == 1).all()) and bool((src[0] == 1).all())
 
 
 def test_gemm_nothing_along_k():

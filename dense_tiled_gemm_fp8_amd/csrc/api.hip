@@ -823,7 +823,8 @@ gemm355_status norm_setup(const gemm355_rmsnorm_args *a, NormParams &p)
     if (!a || a->rows < 0 || a->width < 0) return GEMM355_EINVAL;
     if (!known(a->x_type) || !known(a->r_type) || !known(a->w_type) || !known(a->y_type)) return GEMM355_EINVAL;
     if (!(a->eps > 0.0f) || !(a->eps < INFINITY)) return GEMM355_EINVAL;
-    if (a->rows > ((int64_t)1 << 22) || a->width > ((int64_t)1 << 15)) return GEMM355_EUNSUPPORTED;
+    /* a workgroup of 1024 threads a row, fewer than 2^32 of them */
+    if (a->rows >= ((int64_t)1 << 22) || a->width > ((int64_t)1 << 15)) return GEMM355_EUNSUPPORTED;
     const int64_t n = a->rows, k = a->width;
     const Rows x(a->x, n, k, a->ldx, a->x_type), r(a->residual, n, k, a->ldr, a->r_type), h(a->sum, n, k, a->lds, a->r_type),
         y(a->y, n, k, a->ldy, a->y_type);

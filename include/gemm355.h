@@ -819,7 +819,7 @@ GEMM355_API gemm355_status gemm355_block_quantize(const void *x, int64_t ld, gem
  * One kernel, no scratch; rows or width = 0: nothing is done.
  * Errors: EINVAL (sizes, enums, null pointers, overlaps, eps not above 0 or not
  * finite, q's sizes or its block_rows not 1), EALIGN (pointers to their element),
- * EUNSUPPORTED (rows above 2^22, width above 2^15, ld* above 2^30), EHIP.
+ * EUNSUPPORTED (rows above 2^22 - 1, width above 2^15, ld* above 2^30), EHIP.
  */
 typedef struct gemm355_rmsnorm_args {
     int64_t rows, width;

@@ -123,6 +123,11 @@ def test_norm_refused(change, want):
     assert status(g.gemm355_rmsnorm, norm(**change)) == want
 
 
+def test_norm_rows_whose_threads_reach_32_bits():
+    # 2^22 rows of 1024 threads are one more than a launch counts
+    assert status(g.gemm355_rmsnorm, norm(rows=1 << 22, width=8192)) == g.EUNSUPPORTED
+
+
 def test_nothing_to_do():
     """Sizes of zero return before any launch (there may be no device)."""
     for m in (matrix(rows=0), matrix(K=0), matrix(rows=0, K=0, codes=None, scales=None)):
